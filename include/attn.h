@@ -58,7 +58,8 @@ typedef enum {
     ATTN_ERR_ALIGN = 5,          /* a pointer is not 16-byte aligned               */
     ATTN_ERR_WORKSPACE = 6,      /* workspace NULL or smaller than required        */
     ATTN_ERR_CUDA = 7,           /* the CUDA runtime reported an error             */
-    ATTN_ERR_DEVICE_TIMEOUT = 8  /* a kernel gave up a bounded wait (see below)    */
+    ATTN_ERR_DEVICE_TIMEOUT = 8, /* a kernel gave up a bounded wait (see below)    */
+    ATTN_ERR_ALIAS = 9           /* an output overlaps another argument (cache calls) */
 } attn_status_t;
 
 typedef enum { ATTN_F32 = 0, ATTN_BF16 = 1 } attn_dtype_t;
@@ -242,7 +243,11 @@ typedef enum {
     ATTN_KERNEL_FWD_F32X = 9,     /* tcgen05 forward, fp32 by bf16 pieces      */
     ATTN_KERNEL_BWD_F32X = 10,    /* ... backward: dK/dV and dQ passes, one launch */
     ATTN_KERNEL_BWD_KV = 11,      /* tcgen05 dK/dV pass (ATTN_DQ_SEPARATE)      */
-    ATTN_KERNEL_BWD_DQ = 12       /* tcgen05 dQ pass (ATTN_DQ_SEPARATE)         */
+    ATTN_KERNEL_BWD_DQ = 12,      /* tcgen05 dQ pass (ATTN_DQ_SEPARATE)         */
+    ATTN_KERNEL_DECODE_SIMT = 13, /* CUDA-core decode over a paged cache       */
+    ATTN_KERNEL_DECODE_JOIN = 14, /* joins the pieces of split decode items    */
+    ATTN_KERNEL_CACHE_BOOKS = 15, /* table, lengths and counts of a cache call */
+    ATTN_KERNEL_CACHE_ROWS = 16   /* the rows that a cache call writes or moves */
 } attn_kernel_id_t;
 
 typedef struct {
@@ -304,6 +309,122 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
                                void* workspace, size_t workspace_bytes, int B, int n,
                                int d_model, int H, int dv, attn_dtype_t dtype, void* stream);
 
+/*
+ * Paged key-value cache: answering token by token.
+ *
+ * A cache keeps the keys and values of B sequences in pages of `page` tokens,
+ * so that sequences grow, end, share a prefix and roll back without moving:
+ *   K_pages [num_pages, Hkv, page, d], V_pages [num_pages, Hkv, page, dv]
+ *           the pools, of the element type
+ *   table   [B, max_pages]  page numbers: token t of sequence b is row
+ *           t % page of page table[b][t / page]
+ *   lens    [B]  tokens of each sequence
+ *   ref     [num_pages]  references to each page; a page is free at 0
+ * table, lens and ref are int32 in device memory, 4-byte aligned, and the
+ * caller's: a new cache is lens = 0 and ref = 0. Every sequence holds one
+ * reference to each of its ceil(lens / page) pages. The caller may hold
+ * references of its own (a kept prefix) by counting ref up while no call is in
+ * flight. Entries of a table row past the sequence's pages mean nothing.
+ *
+ * The head count Hkv of the pools may be smaller than the H of the queries:
+ * query head h reads key head h / (H / Hkv).
+ *
+ * Conventions beyond those of the other calls:
+ *  - page is a power of two, 8 to 256; d, dv <= 128 (ATTN_ERR_UNSUPPORTED
+ *    beyond) with rows of whole 16 bytes (multiples of 8 in bf16, of 4 in
+ *    fp32; ATTN_ERR_SHAPE otherwise). num_pages * Hkv, B * max_pages and
+ *    max_pages * page are below 2^31.
+ *  - Nothing is read back to the host: every call can be captured in a graph
+ *    and replayed. What a call finds on the device is checked there. Lengths
+ *    are clamped to [0, max_pages * page]. A page number outside
+ *    [0, num_pages) is never followed: its tokens are masked (attn_decode),
+ *    or the entry is carried along (the others).
+ *  - attn_cache_append, _fork and _compact write table_out, lens_out and
+ *    ref_out, which may each be the same array as the input (in place) and may
+ *    not overlap anything else (ATTN_ERR_ALIAS). Pages are taken lowest
+ *    number first, so results do not depend on timing. Pages of the pools
+ *    are written in place. `info` [3] int32 in device memory receives
+ *      [0] 0: done. 1: not enough free pages. 2: a sequence would outgrow its
+ *          table row. 3: (append) a partly filled last page is not the
+ *          sequence's alone. In cases 1 to 3 the call changes nothing: the
+ *          outputs are copies of the inputs, and no page is written
+ *      [1] free pages after the call
+ *      [2] pages taken (append), copied (fork) or moved (compact)
+ *  - A workspace belongs to one call in flight; contents on entry do not
+ *    matter. Calls that change a cache and calls that read it are ordered by
+ *    the caller, by one stream or events.
+ */
+
+/*
+ * attn_decode -- attention of the newest n tokens of every sequence (n = 1: the
+ * step of token-by-token answering; more: a draft to be checked, a short
+ * continuation) over its cache. Their own keys and values are in the cache
+ * already (attn_cache_append). For sequence b with L = lens[b] tokens and
+ * c = q_len[b] queries (clamped to [0, n]; q_len NULL: n everywhere):
+ *   S_ij = scale * Q_i . K_j,  S_ij = -inf for j >= L, and, if causal, for
+ *          j >= L - (c - 1 - i): query i is token L - c + i
+ *   P = softmax(S),  O = P V,  LSE_i = log sum_j exp(S_ij)
+ *   Q [B,H,n,d], O [B,H,n,dv] element type; LSE [B,H,n] fp32.
+ * A query that sees no key (an empty sequence) gets O = 0 and LSE = -inf. Rows
+ * i >= q_len[b] of O and LSE are left as they were. What unused rows of a page
+ * hold (NaN included) has no influence. H must be a multiple of Hkv.
+ * Pieces of a long sequence are joined in a fixed order: a repeated call gives
+ * the same bits. Whole prompts belong to attn_fwd.
+ */
+size_t attn_decode_workspace_size(int B, int H, int Hkv, int n, int d, int dv, attn_dtype_t dtype);
+attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_pages, const int* table,
+                          const int* lens, const int* q_len, void* O, float* LSE, void* workspace,
+                          size_t workspace_bytes, int B, int H, int Hkv, int n, int d, int dv,
+                          int num_pages, int page, int max_pages, attn_dtype_t dtype, int causal,
+                          float scale, void* stream);
+
+/* Workspace of attn_cache_append, _fork and _compact. 0 if a size is invalid. */
+size_t attn_cache_workspace_size(int B, int max_pages, int num_pages);
+
+/*
+ * attn_cache_append -- new tokens into the cache.
+ *   K [B,Hkv,n,d], V [B,Hkv,n,dv]: the keys and values that attn_fwd or
+ *   attn_decode takes. Rows i < new_len[b] (clamped to [0, n]; NULL: n) become
+ *   tokens lens[b] + i; the others are padding. Pages are taken for sequence
+ *   0 first, then 1, and so on.
+ */
+attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, void* V_pages,
+                                const int* table, const int* lens, const int* ref, const int* new_len,
+                                int* table_out, int* lens_out, int* ref_out, int* info, void* workspace,
+                                size_t workspace_bytes, int B, int Hkv, int n, int d, int dv,
+                                int num_pages, int page, int max_pages, attn_dtype_t dtype, void* stream);
+
+/*
+ * attn_cache_fork -- sequence b becomes the first keep[b] tokens of sequence
+ * src[b], all at once (keep clamped to [0, lens[src[b]]]; NULL: all of them).
+ *   src[b] == b, all kept   b stays
+ *   src[b] == b, fewer      b rolls back (a rejected draft)
+ *   src[b] == another       a fork, a beam's new parent, a shared prefix
+ *   src[b] outside [0, B)   b ends: its pages are given up, its length is 0
+ * Full pages are shared (one more reference each). A partly filled last page
+ * has one holder: it stays with the sequence it belonged to (else with the
+ * lowest of those that continue it) if nothing else refers to it, and is
+ * copied to a fresh page for every other. Entries of table_out that a sequence
+ * gives up are -1.
+ */
+attn_status_t attn_cache_fork(void* K_pages, void* V_pages, const int* table, const int* lens,
+                              const int* ref, const int* src, const int* keep, int* table_out,
+                              int* lens_out, int* ref_out, int* info, void* workspace,
+                              size_t workspace_bytes, int B, int Hkv, int d, int dv, int num_pages,
+                              int page, int max_pages, attn_dtype_t dtype, void* stream);
+
+/*
+ * attn_cache_compact -- the live pages to the front of the pools, so that what
+ * lies behind them can be given back. With L pages live, the k-th live page at
+ * or past L moves to the k-th free page before L.
+ *   remap [num_pages] int32 (written): the new number of each page, -1 if it
+ *   is free; for references that the caller holds itself. lens is only read.
+ */
+attn_status_t attn_cache_compact(void* K_pages, void* V_pages, const int* table, const int* lens,
+                                 const int* ref, int* table_out, int* ref_out, int* remap, int* info,
+                                 void* workspace, size_t workspace_bytes, int B, int Hkv, int d, int dv,
+                                 int num_pages, int page, int max_pages, attn_dtype_t dtype, void* stream);
+
 /* Select the kernel path for the calling thread's later calls (see
  * attn_path_t). */
 attn_status_t attn_set_path(attn_path_t path);
@@ -313,7 +434,7 @@ attn_status_t attn_set_path(attn_path_t path);
 attn_status_t attn_set_dq_path(attn_dq_path_t path);
 
 /* Number of kernels the calling thread's last successful attn_fwd/attn_bwd/
- * attn_proj_bwd/attn_outproj_bwd call launched. */
+ * attn_proj_bwd/attn_outproj_bwd/attn_decode/attn_cache_* call launched. */
 int attn_last_launch_count(void);
 
 /* A static, human-readable name for a status code. */

@@ -26,6 +26,8 @@ __all__ = [
     "attn_bwd_noalloc", "attn_bwd_noalloc_scratch_bytes",
     "attn_proj_bwd", "attn_proj_bwd_workspace_size",
     "attn_outproj_bwd", "attn_outproj_bwd_workspace_size",
+    "attn_decode", "attn_decode_workspace_size", "attn_cache_workspace_size",
+    "attn_cache_append", "attn_cache_fork", "attn_cache_compact",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn.so")
@@ -38,7 +40,8 @@ ATTN_ERR_DEVICE_TIMEOUT = 8
 
 KERNEL_NAMES = {1: "fwd_tensor", 2: "fwd_simt", 3: "preprocess", 4: "bwd_tensor",
                 5: "bwd_simt", 6: "finalize", 7: "proj_gather", 8: "gemm",
-                9: "fwd_f32x", 10: "bwd_f32x", 11: "bwd_kv", 12: "bwd_dq"}
+                9: "fwd_f32x", 10: "bwd_f32x", 11: "bwd_kv", 12: "bwd_dq",
+                13: "decode_simt", 14: "decode_join", 15: "cache_books", 16: "cache_rows"}
 
 
 class _KernelTime(ctypes.Structure):
@@ -108,6 +111,18 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.attn_outproj_bwd_workspace_size.restype = sz
     L.attn_outproj_bwd.argtypes = [vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, i, vp]
     L.attn_outproj_bwd.restype = i
+    L.attn_decode_workspace_size.argtypes = [i, i, i, i, i, i, i]
+    L.attn_decode_workspace_size.restype = sz
+    L.attn_decode.argtypes = [vp] * 9 + [sz] + [i] * 11 + [f, vp]
+    L.attn_decode.restype = i
+    L.attn_cache_workspace_size.argtypes = [i, i, i]
+    L.attn_cache_workspace_size.restype = sz
+    L.attn_cache_append.argtypes = [vp] * 13 + [sz] + [i] * 9 + [vp]
+    L.attn_cache_append.restype = i
+    L.attn_cache_fork.argtypes = [vp] * 12 + [sz] + [i] * 8 + [vp]
+    L.attn_cache_fork.restype = i
+    L.attn_cache_compact.argtypes = [vp] * 10 + [sz] + [i] * 8 + [vp]
+    L.attn_cache_compact.restype = i
     return L
 
 
@@ -345,3 +360,192 @@ def attn_outproj_bwd(o, wo, g, workspace=None, do=None, dwo=None, stream=None):
                                 B, n, d_model, H, dvw, code, _stream_handle(stream)),
            "attn_outproj_bwd")
     return do, dwo
+
+
+# ------------------------------------------------------ paged key-value cache
+def _out(t, name, shape, dtype, device):
+    """An output the caller passed, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape)
+            or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _ints(t, name, shape, device):
+    """An int32 argument on the pools' device (None stays None)."""
+    return None if t is None else _out(t, name, shape, torch.int32, device)
+
+
+def _opt(t) -> ctypes.c_void_p:
+    return ctypes.c_void_p(None if t is None else t.data_ptr())
+
+
+def _bytes(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _pools(k_pages, v_pages, table, lens):
+    """(P, Hkv, page, d, dv, B, M) of a cache, its tensors checked."""
+    _require(k_pages, v_pages)
+    if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
+        raise ValueError("K and V pages must be [P, Hkv, page, d] and [P, Hkv, page, dv] tensors")
+    if v_pages.device != k_pages.device:
+        raise ValueError("K and V pages must live on one device")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be an int32 [B, max_pages] tensor")
+    _ints(table, "table", table.shape, k_pages.device)
+    B, M = table.shape
+    if lens is None:
+        raise ValueError("lens must be an int32 [B] tensor")
+    _ints(lens, "lens", (B,), k_pages.device)
+    P, Hkv, page, d = k_pages.shape
+    return P, Hkv, page, d, v_pages.shape[3], B, M
+
+
+class _On:
+    """The device of a call's tensors and the stream it runs on made current,
+    so that what the binding allocates belongs to that stream."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+        self._device = torch.cuda.device(device)
+        self._stream = torch.cuda.stream(stream)       # None: no change
+
+    def __enter__(self):
+        self._device.__enter__()
+        self._stream.__enter__()
+
+    def __exit__(self, *e):
+        self._stream.__exit__(*e)
+        self._device.__exit__(*e)
+
+
+def attn_decode_workspace_size(B, H, Hkv, n, d, dv, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    return int(lib.attn_decode_workspace_size(B, H, Hkv, n, d, dv, code))
+
+
+def attn_cache_workspace_size(B, max_pages, num_pages) -> int:
+    return int(lib.attn_cache_workspace_size(B, max_pages, num_pages))
+
+
+def attn_decode(q, k_pages, v_pages, table, lens, causal=True, scale=None, q_len=None, out=None,
+                lse=None, workspace=None, stream=None):
+    """Attention of the newest n tokens of every sequence over its pages:
+    returns (O [B,H,n,dv], LSE [B,H,n]) for q [B,H,n,d], pages
+    [P,Hkv,page,d|dv], an int32 table [B,max_pages] and lengths [B], on the
+    device. The new tokens' keys and values are in the cache already. causal:
+    query i of c is token lens[b] - c + i and sees the tokens up to itself.
+    q_len (optional int32 [B]): queries of each sequence; rows past it are left
+    as they were (undefined in an `out` that this call allocates)."""
+    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
+    _require(k_pages, q)
+    dev = k_pages.device
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d or q.device != dev:
+        raise ValueError(f"q must be a [{B}, H, n, {d}] tensor on {dev}")
+    H, n = q.shape[1], q.shape[2]
+    q_len = _ints(q_len, "q_len", (B,), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    code = dtype_code(q.dtype)
+    with _On(dev, stream):
+        out = _out(out, "out", (B, H, n, dvw), q.dtype, dev)
+        lse = _out(lse, "lse", (B, H, n), torch.float32, dev)
+        workspace = _bytes(workspace, attn_decode_workspace_size(B, H, Hkv, n, d, dvw, code), dev)
+        _check(lib.attn_decode(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens),
+                               _opt(q_len), _ptr(out), _ptr(lse), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), B, H, Hkv, n, d, dvw, P,
+                               page, M, code, int(bool(causal)), scale, _stream_handle(None)),
+               "attn_decode")
+    return out, lse
+
+
+def attn_cache_append(k, v, k_pages, v_pages, table, lens, ref, new_len=None, table_out=None,
+                      lens_out=None, ref_out=None, info=None, workspace=None, stream=None):
+    """New tokens k [B,Hkv,n,d], v [B,Hkv,n,dv] into the pages; returns
+    (table, lens, ref, info) after it. Pass table_out=table and so on to work
+    in place. new_len (optional int32 [B]): valid rows of each sequence.
+    info [3]: status (0: done), free pages, pages taken."""
+    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
+    _require(k_pages, k, v)
+    dev = k_pages.device
+    n = k.shape[2] if k.dim() == 4 else 0
+    if (tuple(k.shape) != (B, Hkv, n, d) or tuple(v.shape) != (B, Hkv, n, dvw) or k.device != dev
+            or v.device != dev):
+        raise ValueError(f"k, v must be [{B}, {Hkv}, n, {d}] and [{B}, {Hkv}, n, {dvw}] tensors on {dev}")
+    if ref is None:
+        raise ValueError("ref must be an int32 [P] tensor")
+    _ints(ref, "ref", (P,), dev)
+    new_len = _ints(new_len, "new_len", (B,), dev)
+    with _On(dev, stream):
+        table_out = _out(table_out, "table_out", (B, M), torch.int32, dev)
+        lens_out = _out(lens_out, "lens_out", (B,), torch.int32, dev)
+        ref_out = _out(ref_out, "ref_out", (P,), torch.int32, dev)
+        info = _out(info, "info", (3,), torch.int32, dev)
+        workspace = _bytes(workspace, attn_cache_workspace_size(B, M, P), dev)
+        _check(lib.attn_cache_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(table),
+                                     _ptr(lens), _ptr(ref), _opt(new_len), _ptr(table_out),
+                                     _ptr(lens_out), _ptr(ref_out), _ptr(info), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), B, Hkv, n, d, dvw,
+                                     P, page, M, dtype_code(k.dtype), _stream_handle(None)),
+               "attn_cache_append")
+    return table_out, lens_out, ref_out, info
+
+
+def attn_cache_fork(k_pages, v_pages, table, lens, ref, src, keep=None, table_out=None, lens_out=None,
+                    ref_out=None, info=None, workspace=None, stream=None):
+    """Sequence b becomes the first keep[b] tokens (default: all) of sequence
+    src[b] (int32 [B]; outside [0, B): b ends); returns (table, lens, ref,
+    info) after it. Forks, beam reordering, shared prefixes, roll-back and
+    freeing. info [3]: status (0: done), free pages, pages copied."""
+    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    if ref is None or src is None:
+        raise ValueError("ref must be an int32 [P] tensor and src an int32 [B] tensor")
+    _ints(ref, "ref", (P,), dev)
+    _ints(src, "src", (B,), dev)
+    keep = _ints(keep, "keep", (B,), dev)
+    with _On(dev, stream):
+        table_out = _out(table_out, "table_out", (B, M), torch.int32, dev)
+        lens_out = _out(lens_out, "lens_out", (B,), torch.int32, dev)
+        ref_out = _out(ref_out, "ref_out", (P,), torch.int32, dev)
+        info = _out(info, "info", (3,), torch.int32, dev)
+        workspace = _bytes(workspace, attn_cache_workspace_size(B, M, P), dev)
+        _check(lib.attn_cache_fork(_ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens), _ptr(ref),
+                                   _ptr(src), _opt(keep), _ptr(table_out), _ptr(lens_out), _ptr(ref_out),
+                                   _ptr(info), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), B, Hkv, d, dvw, P, page,
+                                   M, dtype_code(k_pages.dtype), _stream_handle(None)),
+               "attn_cache_fork")
+    return table_out, lens_out, ref_out, info
+
+
+def attn_cache_compact(k_pages, v_pages, table, lens, ref, table_out=None, ref_out=None, remap=None,
+                       info=None, workspace=None, stream=None):
+    """The live pages to the front of the pools; returns (table, ref, remap,
+    info) after it. remap [P]: the new number of each page, -1 if free.
+    info [3]: 0, free pages, pages moved."""
+    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    if ref is None:
+        raise ValueError("ref must be an int32 [P] tensor")
+    _ints(ref, "ref", (P,), dev)
+    with _On(dev, stream):
+        table_out = _out(table_out, "table_out", (B, M), torch.int32, dev)
+        ref_out = _out(ref_out, "ref_out", (P,), torch.int32, dev)
+        remap = _out(remap, "remap", (P,), torch.int32, dev)
+        info = _out(info, "info", (3,), torch.int32, dev)
+        workspace = _bytes(workspace, attn_cache_workspace_size(B, M, P), dev)
+        _check(lib.attn_cache_compact(_ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens), _ptr(ref),
+                                      _ptr(table_out), _ptr(ref_out), _ptr(remap), _ptr(info),
+                                      _ptr(workspace), workspace.numel() * workspace.element_size(), B,
+                                      Hkv, d, dvw, P, page, M, dtype_code(k_pages.dtype),
+                                      _stream_handle(None)),
+               "attn_cache_compact")
+    return table_out, ref_out, remap, info

@@ -23,6 +23,8 @@
 #include "gemm_tc.cuh"
 #include "proj.cuh"
 #include "f32x_tc.cuh"
+#include "decode.cuh"
+#include "cache.cuh"
 
 namespace {
 
@@ -879,8 +881,11 @@ const char* attn_status_string(attn_status_t s) {
         case ATTN_ERR_WORKSPACE: return "workspace missing or too small";
         case ATTN_ERR_CUDA: return "CUDA runtime error";
         case ATTN_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
+        case ATTN_ERR_ALIAS: return "arguments overlap in memory";
     }
     return "unknown status";
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

@@ -1,0 +1,216 @@
+// decode.cuh -- attention of the newest tokens of every sequence over its
+// paged keys and values, on the CUDA cores, and the joining of split items.
+//
+//   S_rj = scale * q_r . k_j  over the keys j that row r may see,
+//   O_r = sum_j softmax(S_r)_j v_j,  LSE_r = ln sum_j exp(S_rj)
+//
+// A row that sees no key gets O = 0 and LSE = -inf. Query rows of one key head
+// (its group of query heads, times the new tokens) are taken together, so that
+// every key and value is read once for all of them. One pass over the keys
+// with a running maximum and sum per row (base 2, fp32).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "paged.cuh"
+#include "simt.cuh"
+#include "sm100.cuh"
+
+namespace attn {
+namespace paged {
+
+constexpr int kRows = 16;             // query rows per item
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxWidth = 128;
+
+// Last key (exclusive) that query i of nq sees in a sequence of len tokens,
+// the queries being its last nq tokens.
+__device__ __forceinline__ int visible(const DecodeArgs& a, int len, int nq, int i) {
+    return a.causal ? len - (nq - 1 - i) : len;
+}
+
+// Rows of an item are numbered r = g * n + i (query head hk * G + g, query i),
+// which are consecutive rows of Q, O and LSE.
+__device__ __forceinline__ size_t row_base(const DecodeArgs& a, int b, int hk) {
+    return (size_t(b) * a.H + size_t(hk) * (a.H / a.g.Hkv)) * a.n;
+}
+
+constexpr int kSimtThreads = 128;
+
+__host__ __device__ constexpr int simt_smem_bytes(int d, int dv) {
+    return (kRows * d + kTileKeys * (d + 1) + kTileKeys * dv + kRows * kTileKeys + 3 * kRows) * 4;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads)
+decode_simt(DecodeArgs a, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
+            T* __restrict__ O, float* __restrict__ LSE, Parts parts) {
+    extern __shared__ float sm[];
+    __shared__ long long scratch[33], found[2];
+    __shared__ int pages[kTileKeys];
+    const int d = a.d, dv = a.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float* Qs = sm;                              // [16][d]
+    float* Ks = Qs + kRows * d;                  // [64][d + 1]
+    float* Vs = Ks + kTileKeys * (d + 1);        // [64][dv]
+    float* Ps = Vs + kTileKeys * dv;             // [16][64]
+    float* Ms = Ps + kRows * kTileKeys;          // [16] maximum
+    float* Ls = Ms + kRows;                      // [16] sum
+    float* Cs = Ls + kRows;                      // [16] factor of the old sums
+
+    Walker w;
+    w.start(a, scratch, found);
+    if (tid == 0) parts.head[blockIdx.x].b = -1;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    const int page = 1 << a.g.page_log2;
+
+    Piece p;
+    while (w.next(a, &p)) {
+        const int hk = p.item / a.row_tiles, r0 = (p.item % a.row_tiles) * kRows;
+        const int rows = min(kRows, a.rows - r0);
+        const size_t base = row_base(a, p.b, hk) + r0;
+        __syncthreads();
+        for (int x = tid; x < rows * d; x += kSimtThreads) Qs[x] = simt::to_f(Q[base * d + x]);
+        if (tid < kRows) {
+            Ms[tid] = -INFINITY;
+            Ls[tid] = 0.f;
+        }
+        float acc[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) acc[r] = 0.f;
+
+        for (int t = p.t0; t < p.t1; ++t) {
+            const int k0 = t * kTileKeys;
+            __syncthreads();
+            if (tid < kTileKeys) {
+                const int j = k0 + tid;
+                int pg = -1;
+                if (j < p.len) {
+                    pg = a.table[size_t(p.b) * a.g.M + (j >> a.g.page_log2)];
+                    if (!page_ok(pg, a.g.P)) pg = -1;
+                }
+                pages[tid] = pg;
+            }
+            __syncthreads();
+            // Rows of absent tokens are zeros: their weight is zero, and zero
+            // times what an unused row may hold need not be.
+            for (int j = warp; j < kTileKeys; j += kSimtThreads / 32) {
+                const int pg = pages[j];
+                const size_t row = (size_t(max(pg, 0)) * a.g.Hkv + hk) * page + ((k0 + j) & (page - 1));
+                for (int c = lane; c < d; c += 32) Ks[j * (d + 1) + c] = pg >= 0 ? simt::to_f(Kp[row * d + c]) : 0.f;
+                for (int c = lane; c < dv; c += 32) Vs[j * dv + c] = pg >= 0 ? simt::to_f(Vp[row * dv + c]) : 0.f;
+            }
+            __syncthreads();
+            {
+                const int j = tid & 63;
+                const bool there = pages[j] >= 0;
+                for (int r = tid >> 6; r < rows; r += 2) {
+                    float s = 0.f;
+                    for (int c = 0; c < d; ++c) s = fmaf(Qs[r * d + c], Ks[j * (d + 1) + c], s);
+                    const bool see = there && k0 + j < visible(a, p.len, p.nq, (r0 + r) % a.n);
+                    Ps[r * kTileKeys + j] = see ? s * scale_log2 : -INFINITY;
+                }
+            }
+            __syncthreads();
+            for (int r = warp; r < rows; r += kSimtThreads / 32) {
+                const float s0 = Ps[r * kTileKeys + lane], s1 = Ps[r * kTileKeys + 32 + lane];
+                const float old = Ms[r];
+                const float m = fmaxf(old, simt::warp_max(fmaxf(s0, s1)));
+                const float ms = m == -INFINITY ? 0.f : m;     // a row without keys so far
+                const float e0 = exp2f(s0 - ms), e1 = exp2f(s1 - ms), c = exp2f(old - ms);
+                const float sum = simt::warp_sum(e0 + e1);
+                Ps[r * kTileKeys + lane] = e0;
+                Ps[r * kTileKeys + 32 + lane] = e1;
+                __syncwarp();
+                if (lane == 0) {
+                    Ms[r] = m;
+                    Ls[r] = Ls[r] * c + sum;
+                    Cs[r] = c;
+                }
+            }
+            __syncthreads();
+            if (tid < dv) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    if (r < rows) {
+                        float s = acc[r] * Cs[r];
+                        for (int j = 0; j < kTileKeys; ++j) s = fmaf(Ps[r * kTileKeys + j], Vs[j * dv + tid], s);
+                        acc[r] = s;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = p.t0 == 0 && p.t1 == p.tiles;
+        const size_t slot = 2 * size_t(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
+        if (whole) {
+            if (tid < dv) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (r < rows && (r0 + r) % a.n < p.nq)
+                        O[(base + r) * dv + tid] = simt::from_f<T>(Ls[r] > 0.f ? acc[r] / Ls[r] : acc[r]);
+            }
+            if (tid < rows && (r0 + tid) % a.n < p.nq)
+                LSE[base + tid] = (Ms[tid] + log2f(Ls[tid])) * kLn2;
+        } else {
+            if (tid < dv) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (r < rows) parts.o[(slot * kRows + r) * dv + tid] = acc[r];
+            }
+            if (tid < rows) {
+                parts.ml[(slot * kRows + tid) * 2] = Ms[tid];
+                parts.ml[(slot * kRows + tid) * 2 + 1] = Ls[tid];
+            }
+            if (tid == 0 && p.t0 == 0) {
+                Head h;
+                h.b = p.b;
+                h.item = p.item;
+                h.nq = p.nq;
+                h.last = w.owner(p.end - 1);
+                parts.head[blockIdx.x] = h;
+            }
+        }
+    }
+}
+
+// One warp per row of the item that starts in CTA blockIdx.x and goes on:
+// O = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over its pieces, in the
+// order of the CTAs, so that a repeated call gives the same bits.
+constexpr int kJoinThreads = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads)
+decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts parts) {
+    const Head h = parts.head[blockIdx.x];
+    if (h.b < 0) return;
+    const int hk = h.item / a.row_tiles, r0 = (h.item % a.row_tiles) * kRows;
+    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= min(kRows, a.rows - r0) || (r0 + r) % a.n >= h.nq) return;
+    const int first = blockIdx.x;
+    float m = -INFINITY;
+    for (int c = first + lane; c <= h.last; c += 32) {
+        const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
+        m = fmaxf(m, parts.ml[(slot * kRows + r) * 2]);
+    }
+    m = simt::warp_max(m);
+    const float ms = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[kMaxWidth / 32] = {};
+    for (int c = first; c <= h.last; ++c) {
+        const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
+        const float f = exp2f(parts.ml[(slot * kRows + r) * 2] - ms);
+        l = fmaf(parts.ml[(slot * kRows + r) * 2 + 1], f, l);
+#pragma unroll
+        for (int k = 0; k < kMaxWidth / 32; ++k)
+            if (lane + 32 * k < a.dv) acc[k] = fmaf(parts.o[(slot * kRows + r) * a.dv + lane + 32 * k], f, acc[k]);
+    }
+    const size_t row = row_base(a, h.b, hk) + r0 + r;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxWidth / 32; ++k)
+        if (lane + 32 * k < a.dv) O[row * a.dv + lane + 32 * k] = simt::from_f<T>(acc[k] * inv);
+    if (lane == 0) LSE[row] = (m + log2f(l)) * kLn2;
+}
+
+}  // namespace paged
+}  // namespace attn

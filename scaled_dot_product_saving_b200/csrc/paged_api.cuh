@@ -1,0 +1,342 @@
+// paged_api.cuh -- the entry points of the paged key-value cache (part of the
+// one translation unit that attn.cu compiles): argument checks, workspaces and
+// launches of decode.cuh and cache.cuh.
+#pragma once
+
+namespace {
+
+namespace pg = attn::paged;
+
+constexpr int kDecodeCtas = 444;        // most CTAs of a decode call (workspace slots)
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Bytes [p, p + n) that a call reads or writes.
+struct Region {
+    const void* p;
+    size_t n;
+};
+inline bool overlap(const Region& a, const Region& b) {
+    const char* x = static_cast<const char*>(a.p);
+    const char* y = static_cast<const char*>(b.p);
+    return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
+}
+// No written region may touch another written or read one. in_place holds the
+// read regions that the written region of the same index may equal.
+template <size_t W, size_t R>
+bool apart(const Region (&written)[W], const Region (&read)[R], const Region* in_place, size_t pairs) {
+    for (size_t i = 0; i < W; ++i) {
+        for (size_t j = i + 1; j < W; ++j)
+            if (overlap(written[i], written[j])) return false;
+        for (size_t j = 0; j < R; ++j)
+            if (overlap(written[i], read[j])) return false;
+        for (size_t j = 0; j < pairs; ++j)
+            if (overlap(written[i], in_place[j]) && !(i == j && written[i].p == in_place[j].p)) return false;
+    }
+    return true;
+}
+
+attn_status_t check_cache(int B, int Hkv, int d, int dv, int num_pages, int page, int max_pages,
+                          attn_dtype_t dtype, pg::Geometry* g) {
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
+    if (B < 1 || Hkv < 1 || d < 1 || dv < 1 || num_pages < 1 || page < 1 || max_pages < 1)
+        return ATTN_ERR_SHAPE;
+    int log2 = 0;
+    while ((1 << log2) < page && log2 < 30) ++log2;
+    if ((1 << log2) != page || log2 < pg::kMinPageLog2 || log2 > pg::kMaxPageLog2) return ATTN_ERR_UNSUPPORTED;
+    if (d > pg::kMaxWidth || dv > pg::kMaxWidth) return ATTN_ERR_UNSUPPORTED;
+    const int es = dtype == ATTN_F32 ? 4 : 2;
+    if (d * es % 16 || dv * es % 16) return ATTN_ERR_SHAPE;
+    if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) ||
+        static_cast<long long>(B) * max_pages >= (1ll << 31) || max_pages > (0x7fffffff >> log2))
+        return ATTN_ERR_SHAPE;
+    *g = pg::Geometry{B, max_pages, num_pages, Hkv, log2};
+    return ATTN_OK;
+}
+
+size_t pool_bytes(const pg::Geometry& g, int width, attn_dtype_t dtype) {
+    return (static_cast<size_t>(g.P) * g.Hkv << g.page_log2) * width * (dtype == ATTN_F32 ? 4 : 2);
+}
+
+// ------------------------------------------------------------------ decode
+struct DecodeWorkspace {
+    size_t o_off, ml_off, head_off, total;
+};
+DecodeWorkspace carve_decode(int dv) {
+    DecodeWorkspace w;
+    const size_t rows = 2ull * kDecodeCtas * pg::kRows;
+    w.o_off = 0;
+    w.ml_off = round_up(rows * dv * sizeof(float), 256);
+    w.head_off = w.ml_off + round_up(rows * 2 * sizeof(float), 256);
+    w.total = w.head_off + round_up(kDecodeCtas * sizeof(pg::Head), 256);
+    return w;
+}
+
+attn_status_t check_decode(int B, int H, int Hkv, int n, int d, int dv, attn_dtype_t dtype) {
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
+    if (B < 1 || H < 1 || Hkv < 1 || n < 1 || d < 1 || dv < 1 || H % Hkv) return ATTN_ERR_SHAPE;
+    if (static_cast<double>(B) * H * n >= 2147483648.0) return ATTN_ERR_SHAPE;
+    if (d > pg::kMaxWidth || dv > pg::kMaxWidth) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+template <typename T>
+attn_status_t decode_simt(const pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O,
+                          float* LSE, const pg::Parts& parts, int grid, cudaStream_t st) {
+    const int smem = pg::simt_smem_bytes(a.d, a.dv);
+    auto kern = pg::decode_simt<T>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    return traced(ATTN_KERNEL_DECODE_SIMT, st, [&] {
+        kern<<<grid, pg::kSimtThreads, smem, st>>>(a, static_cast<const T*>(Q), static_cast<const T*>(Kp),
+                                                   static_cast<const T*>(Vp), static_cast<T*>(O), LSE, parts);
+        return launched();
+    });
+}
+
+template <typename T>
+attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg::Parts& parts, int grid,
+                          cudaStream_t st) {
+    const int rows = std::min(a.rows, pg::kRows);
+    const dim3 blocks(grid, (rows + pg::kJoinThreads / 32 - 1) / (pg::kJoinThreads / 32));
+    return traced(ATTN_KERNEL_DECODE_JOIN, st, [&] {
+        pg::decode_join<T><<<blocks, pg::kJoinThreads, 0, st>>>(a, static_cast<T*>(O), LSE, parts);
+        return launched();
+    });
+}
+
+// ------------------------------------------------------------------- books
+struct CacheWorkspace {
+    size_t first_off, after_off, start_off, base_off, key_off, stage_off, moves_off, total;
+};
+CacheWorkspace carve_cache(int B, int max_pages, int num_pages) {
+    CacheWorkspace w;
+    const auto ints = [](size_t n) { return round_up(n * sizeof(int), 256); };
+    w.first_off = ints(pg::kCtlWords);
+    w.after_off = w.first_off + ints(static_cast<size_t>(B) + 1);
+    w.start_off = w.after_off + ints(B);
+    w.base_off = w.start_off + ints(B);
+    w.key_off = w.base_off + ints(num_pages);
+    w.stage_off = w.key_off + ints(num_pages);
+    w.moves_off = w.stage_off + ints(static_cast<size_t>(B) * max_pages);
+    w.total = w.moves_off + round_up(std::max<size_t>(B, num_pages) * sizeof(pg::Move), 256);
+    return w;
+}
+
+pg::Books books(const pg::Geometry& g, const int* table, const int* lens, const int* ref, int* table_out,
+                int* lens_out, int* ref_out, int* info, void* workspace) {
+    const CacheWorkspace w = carve_cache(g.B, g.M, g.P);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const auto at = [&](size_t off) { return reinterpret_cast<int*>(ws + off); };
+    return pg::Books{g, table, lens, ref, table_out, lens_out, ref_out, info, at(0), at(w.first_off),
+                     at(w.after_off), at(w.start_off), at(w.base_off), at(w.key_off), at(w.stage_off),
+                     reinterpret_cast<pg::Move*>(ws + w.moves_off)};
+}
+
+// One cluster of kBookCtas CTAs.
+template <typename... P, typename... A>
+attn_status_t launch_books(void (*kern)(P...), cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(pg::kBookCtas);
+    cfg.blockDim = dim3(pg::kBookThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = pg::kBookCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return traced(ATTN_KERNEL_CACHE_BOOKS, st, [&] {
+        if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return ATTN_ERR_CUDA;
+        }
+        return launched();
+    });
+}
+
+attn_status_t launch_moves(const pg::Books& k, void* Kp, void* Vp, int wk, int wv, long long most,
+                           cudaStream_t st) {
+    const int grid = grid_for(static_cast<size_t>(most), 1, sm_count() * 8);
+    return traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
+        pg::move_rows<<<grid, pg::kCopyThreads, 0, st>>>(k.g, static_cast<uint4*>(Kp), static_cast<uint4*>(Vp),
+                                                        k.control, k.moves, wk, wv);
+        return launched();
+    });
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_decode_workspace_size(int B, int H, int Hkv, int n, int d, int dv, attn_dtype_t dtype) {
+    if (check_decode(B, H, Hkv, n, d, dv, dtype) != ATTN_OK) return 0;
+    return carve_decode(dv).total;
+}
+
+attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_pages, const int* table,
+                          const int* lens, const int* q_len, void* O, float* LSE, void* workspace,
+                          size_t workspace_bytes, int B, int H, int Hkv, int n, int d, int dv,
+                          int num_pages, int page, int max_pages, attn_dtype_t dtype, int causal,
+                          float scale, void* stream) {
+    pg::Geometry g;
+    attn_status_t s = check_decode(B, H, Hkv, n, d, dv, dtype);
+    if (s == ATTN_OK) s = check_cache(B, Hkv, d, dv, num_pages, page, max_pages, dtype, &g);
+    if (s != ATTN_OK) return s;
+    if (!std::isfinite(scale)) return ATTN_ERR_SHAPE;
+    if (!Q || !K_pages || !V_pages || !table || !lens || !O || !LSE) return ATTN_ERR_NULL;
+    if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O) || !aligned16(LSE) ||
+        !aligned4(table) || !aligned4(lens) || !aligned4(q_len))
+        return ATTN_ERR_ALIGN;
+    const DecodeWorkspace w = carve_decode(dv);
+    if (!workspace || workspace_bytes < w.total) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+
+    pg::DecodeArgs a{g, table, lens, q_len, H, n, d, dv, H / Hkv * n, 0, causal != 0, scale};
+    a.row_tiles = (a.rows + pg::kRows - 1) / pg::kRows;
+    // The kernel numbers its units (key tiles of all items) times CTAs in 64 bits.
+    if (static_cast<double>(B) * Hkv * a.row_tiles * ((static_cast<double>(max_pages) * page) / pg::kTileKeys + 1) >=
+        9007199254740992.0)
+        return ATTN_ERR_SHAPE;
+    const size_t es = dtype == ATTN_F32 ? 4 : 2, rows = static_cast<size_t>(B) * H * n;
+    const Region written[] = {{O, rows * dv * es}, {LSE, rows * 4}, {workspace, w.total}};
+    const Region read[] = {{Q, rows * d * es}, {K_pages, pool_bytes(g, d, dtype)},
+                           {V_pages, pool_bytes(g, dv, dtype)}, {table, static_cast<size_t>(B) * max_pages * 4},
+                           {lens, static_cast<size_t>(B) * 4}, {q_len, static_cast<size_t>(B) * 4}};
+    if (!apart(written, read, nullptr, 0)) return ATTN_ERR_ALIAS;
+
+    cudaStream_t st = as_stream(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const pg::Parts parts{reinterpret_cast<float*>(ws + w.o_off), reinterpret_cast<float*>(ws + w.ml_off),
+                          reinterpret_cast<pg::Head*>(ws + w.head_off)};
+    const int grid = std::min(2 * sm_count(), kDecodeCtas);
+    if (dtype == ATTN_F32) {
+        s = decode_simt<float>(a, Q, K_pages, V_pages, O, LSE, parts, grid, st);
+        if (s == ATTN_OK) s = decode_join<float>(a, O, LSE, parts, grid, st);
+    } else {
+        s = decode_simt<__nv_bfloat16>(a, Q, K_pages, V_pages, O, LSE, parts, grid, st);
+        if (s == ATTN_OK) s = decode_join<__nv_bfloat16>(a, O, LSE, parts, grid, st);
+    }
+    if (s == ATTN_OK) g_last_launches = 2;
+    return s;
+}
+
+size_t attn_cache_workspace_size(int B, int max_pages, int num_pages) {
+    if (B < 1 || max_pages < 1 || num_pages < 1 || static_cast<long long>(B) * max_pages >= (1ll << 31)) return 0;
+    return carve_cache(B, max_pages, num_pages).total;
+}
+
+attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, void* V_pages, const int* table,
+                                const int* lens, const int* ref, const int* new_len, int* table_out,
+                                int* lens_out, int* ref_out, int* info, void* workspace,
+                                size_t workspace_bytes, int B, int Hkv, int n, int d, int dv, int num_pages,
+                                int page, int max_pages, attn_dtype_t dtype, void* stream) {
+    pg::Geometry g;
+    attn_status_t s = check_cache(B, Hkv, d, dv, num_pages, page, max_pages, dtype, &g);
+    if (s != ATTN_OK) return s;
+    if (n < 1 || static_cast<double>(B) * Hkv * n >= 2147483648.0) return ATTN_ERR_SHAPE;
+    if (!K || !V || !K_pages || !V_pages || !table || !lens || !ref || !table_out || !lens_out || !ref_out || !info)
+        return ATTN_ERR_NULL;
+    if (!aligned16(K) || !aligned16(V) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned4(table) ||
+        !aligned4(lens) || !aligned4(ref) || !aligned4(new_len) || !aligned4(table_out) || !aligned4(lens_out) ||
+        !aligned4(ref_out) || !aligned4(info))
+        return ATTN_ERR_ALIGN;
+    const CacheWorkspace w = carve_cache(B, max_pages, num_pages);
+    if (!workspace || workspace_bytes < w.total) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+    const int es = dtype == ATTN_F32 ? 4 : 2;
+    const size_t rows = static_cast<size_t>(B) * Hkv * n, tb = static_cast<size_t>(B) * max_pages * 4,
+                 lb = static_cast<size_t>(B) * 4, rb = static_cast<size_t>(num_pages) * 4;
+    const Region written[] = {{table_out, tb}, {lens_out, lb}, {ref_out, rb}, {info, 12}, {workspace, w.total},
+                              {K_pages, pool_bytes(g, d, dtype)}, {V_pages, pool_bytes(g, dv, dtype)}};
+    const Region read[] = {{K, rows * d * es}, {V, rows * dv * es}, {new_len, lb}};
+    const Region in_place[] = {{table, tb}, {lens, lb}, {ref, rb}};
+    if (!apart(written, read, in_place, 3)) return ATTN_ERR_ALIAS;
+
+    cudaStream_t st = as_stream(stream);
+    const pg::Books k = books(g, table, lens, ref, table_out, lens_out, ref_out, info, workspace);
+    s = launch_books(pg::append_books, st, k, new_len, n);
+    if (s != ATTN_OK) return s;
+    const int wk = d * es / 16, wv = dv * es / 16;
+    const int grid = grid_for(rows * (wk + wv), pg::kCopyThreads, sm_count() * 8);
+    s = traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
+        pg::append_rows<<<grid, pg::kCopyThreads, 0, st>>>(
+            g, static_cast<const uint4*>(K), static_cast<const uint4*>(V), static_cast<uint4*>(K_pages),
+            static_cast<uint4*>(V_pages), table_out, k.control, k.start, k.after, n, wk, wv);
+        return launched();
+    });
+    if (s == ATTN_OK) g_last_launches = 2;
+    return s;
+}
+
+attn_status_t attn_cache_fork(void* K_pages, void* V_pages, const int* table, const int* lens, const int* ref,
+                              const int* src, const int* keep, int* table_out, int* lens_out, int* ref_out,
+                              int* info, void* workspace, size_t workspace_bytes, int B, int Hkv, int d, int dv,
+                              int num_pages, int page, int max_pages, attn_dtype_t dtype, void* stream) {
+    pg::Geometry g;
+    attn_status_t s = check_cache(B, Hkv, d, dv, num_pages, page, max_pages, dtype, &g);
+    if (s != ATTN_OK) return s;
+    if (B > (1 << 29)) return ATTN_ERR_SHAPE;              // the kernel ranks sequences up to 2 B
+    if (!K_pages || !V_pages || !table || !lens || !ref || !src || !table_out || !lens_out || !ref_out || !info)
+        return ATTN_ERR_NULL;
+    if (!aligned16(K_pages) || !aligned16(V_pages) || !aligned4(table) || !aligned4(lens) || !aligned4(ref) ||
+        !aligned4(src) || !aligned4(keep) || !aligned4(table_out) || !aligned4(lens_out) || !aligned4(ref_out) ||
+        !aligned4(info))
+        return ATTN_ERR_ALIGN;
+    const CacheWorkspace w = carve_cache(B, max_pages, num_pages);
+    if (!workspace || workspace_bytes < w.total) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+    const size_t tb = static_cast<size_t>(B) * max_pages * 4, lb = static_cast<size_t>(B) * 4,
+                 rb = static_cast<size_t>(num_pages) * 4;
+    const Region written[] = {{table_out, tb}, {lens_out, lb}, {ref_out, rb}, {info, 12}, {workspace, w.total},
+                              {K_pages, pool_bytes(g, d, dtype)}, {V_pages, pool_bytes(g, dv, dtype)}};
+    const Region read[] = {{src, lb}, {keep, lb}};
+    const Region in_place[] = {{table, tb}, {lens, lb}, {ref, rb}};
+    if (!apart(written, read, in_place, 3)) return ATTN_ERR_ALIAS;
+
+    cudaStream_t st = as_stream(stream);
+    const pg::Books k = books(g, table, lens, ref, table_out, lens_out, ref_out, info, workspace);
+    s = launch_books(pg::fork_books, st, k, src, keep);
+    const int es = dtype == ATTN_F32 ? 4 : 2;
+    if (s == ATTN_OK)
+        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, static_cast<long long>(B) * Hkv, st);
+    if (s == ATTN_OK) g_last_launches = 2;
+    return s;
+}
+
+attn_status_t attn_cache_compact(void* K_pages, void* V_pages, const int* table, const int* lens,
+                                 const int* ref, int* table_out, int* ref_out, int* remap, int* info,
+                                 void* workspace, size_t workspace_bytes, int B, int Hkv, int d, int dv,
+                                 int num_pages, int page, int max_pages, attn_dtype_t dtype, void* stream) {
+    pg::Geometry g;
+    attn_status_t s = check_cache(B, Hkv, d, dv, num_pages, page, max_pages, dtype, &g);
+    if (s != ATTN_OK) return s;
+    if (!K_pages || !V_pages || !table || !lens || !ref || !table_out || !ref_out || !remap || !info)
+        return ATTN_ERR_NULL;
+    if (!aligned16(K_pages) || !aligned16(V_pages) || !aligned4(table) || !aligned4(lens) || !aligned4(ref) ||
+        !aligned4(table_out) || !aligned4(ref_out) || !aligned4(remap) || !aligned4(info))
+        return ATTN_ERR_ALIGN;
+    const CacheWorkspace w = carve_cache(B, max_pages, num_pages);
+    if (!workspace || workspace_bytes < w.total) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+    const size_t tb = static_cast<size_t>(B) * max_pages * 4, lb = static_cast<size_t>(B) * 4,
+                 rb = static_cast<size_t>(num_pages) * 4;
+    const Region written[] = {{table_out, tb}, {ref_out, rb}, {remap, rb}, {info, 12}, {workspace, w.total},
+                              {K_pages, pool_bytes(g, d, dtype)}, {V_pages, pool_bytes(g, dv, dtype)}};
+    const Region read[] = {{lens, lb}};
+    const Region in_place[] = {{table, tb}, {ref, rb}};
+    if (!apart(written, read, in_place, 2)) return ATTN_ERR_ALIAS;
+
+    cudaStream_t st = as_stream(stream);
+    const pg::Books k = books(g, table, lens, ref, table_out, nullptr, ref_out, info, workspace);
+    s = launch_books(pg::compact_books, st, k, remap);
+    const int es = dtype == ATTN_F32 ? 4 : 2;
+    if (s == ATTN_OK)
+        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, static_cast<long long>(num_pages) * Hkv,
+                         st);
+    if (s == ATTN_OK) g_last_launches = 2;
+    return s;
+}
+
+}  // extern "C"

@@ -1,0 +1,269 @@
+"""attn_decode on the GPU against the float64 oracle, on the rounded inputs.
+
+Bounds, per element, from the arithmetic (u = 2^-24; A = sum_j P_j |v_j|,
+X = max_j scale * sum_c |q_c k_jc|, both from the oracle; L keys):
+  a score is a sum of d products scaled once and taken through exp2: its error
+  is at most (d + 4) u X, plus 4 u for the exponential itself, and enters the
+  weights and their sum once each; the two sums over the keys add L u each:
+    fp32  |dO|   <= A u (2 ((d + 4) X + 4) + 2 L + 16),
+          |dLSE| <= u ((d + 4) X + 4 + L + 16 + 2 |LSE|)
+  in bf16 the weights may be rounded to bf16 before the second product (half a
+  step, 2^-8 of each) and the result is rounded once more:
+    bf16  |dO|   <= 2^-8 (1 + 2^-8) A + 2^-8 |O| + the fp32 terms
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as paged
+from paged_util import DT, numpy_cache, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+lib = pytest.importorskip("scaled_dot_product_saving_b200")
+
+U = 2.0 ** -24
+
+
+def run(dev, q, causal=True, q_len=None, scale=None, **kw):
+    ql = None if q_len is None else torch.tensor(q_len, dtype=torch.int32, device="cuda")
+    o, lse = lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"], causal=causal,
+                             scale=scale, q_len=ql, **kw)
+    torch.cuda.synchronize()
+    assert lib.attn_get_device_error() == 0
+    return o, lse
+
+
+def compare(o, lse, dt, host, q, causal=True, q_len=None, scale=None):
+    table, lens = host["table"], host["lens"]
+    O, LSE, A, X = paged.decode(q.double().cpu().numpy(), host["k_pages"], host["v_pages"], table, lens,
+                                q_len, causal, scale)
+    d, L = q.shape[-1], max(1, int(np.max(lens)))
+    live = ~np.isnan(LSE)
+    empty = np.isneginf(LSE)
+    got, gl = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (got[empty] == 0).all() and np.isneginf(gl[empty]).all()
+    some = live & ~empty
+    x = X[..., None]
+    tol = A * U * (2 * ((d + 4) * x + 4) + 2 * L + 16)
+    if dt == "bf16":
+        tol = tol + 2.0 ** -8 * ((1 + 2.0 ** -8) * A + np.abs(O)) * (1 + 2.0 ** -8)
+    err = np.abs(got - O)
+    assert (err <= tol)[some].all(), f"O: worst error / bound {np.nanmax((err / tol)[some])}"
+    tl = U * ((d + 4) * X + 4 + L + 16 + 2 * np.abs(np.where(empty, 0, LSE)))
+    el = np.abs(np.where(empty, 0, gl) - np.where(empty, 0, LSE))
+    assert (el <= tl)[some].all(), f"LSE: worst error / bound {np.nanmax((el / tl)[some])}"
+    return live
+
+
+CASES = [
+    # lens, H, Hkv, n, d, dv, page, causal, dtype
+    ((1,), 1, 1, 1, 64, 64, 16, True, "bf16"),                       # one token
+    ((0, 1, 2, 63, 64, 65), 8, 2, 1, 128, 128, 16, True, "bf16"),    # an empty sequence; tile borders
+    ((700, 129, 1000), 32, 8, 1, 128, 128, 16, True, "bf16"),
+    ((513, 77), 16, 16, 1, 64, 64, 32, True, "bf16"),                # heads not shared
+    ((300, 5, 64), 16, 1, 1, 128, 128, 64, True, "bf16"),            # one key head for all
+    ((95, 640), 48, 2, 1, 128, 128, 128, True, "bf16"),              # 24 rows per key head
+    ((260, 1), 6, 2, 5, 64, 64, 256, True, "bf16"),                  # a draft; fewer keys than queries
+    ((33, 150), 8, 2, 9, 128, 128, 8, True, "bf16"),                 # 36 rows, the smallest page
+    ((200, 64), 4, 4, 4, 128, 128, 16, False, "bf16"),               # not causal
+    ((150, 90), 6, 3, 2, 40, 72, 16, True, "bf16"),                  # odd widths
+    ((150, 90), 6, 3, 1, 8, 128, 8, True, "bf16"),
+    ((150, 90), 2, 1, 3, 96, 16, 32, True, "bf16"),
+    ((1,), 2, 1, 1, 64, 64, 16, True, "f32"),
+    ((0, 1, 63, 64, 65, 129), 8, 2, 1, 128, 128, 16, True, "f32"),
+    ((700, 129), 20, 4, 1, 64, 64, 16, True, "f32"),
+    ((333, 40), 7, 1, 5, 36, 100, 8, True, "f32"),                   # 35 rows, odd widths
+    ((95, 300), 24, 2, 3, 128, 128, 64, False, "f32"),
+    ((50, 260), 3, 3, 1, 4, 4, 256, True, "f32"),
+]
+
+
+@pytest.mark.parametrize("lens,H,Hkv,n,d,dv,page,causal,dt", CASES)
+def test_decode(lens, H, Hkv, n, d, dv, page, causal, dt):
+    rng = np.random.default_rng(len(lens) * 1000 + d + n)
+    dev, host = on_gpu(numpy_cache(rng, len(lens), Hkv, page, d, dv, lens), dt)
+    q = torch.tensor(rng.standard_normal((len(lens), H, n, d)), device="cuda").to(DT[dt])
+    o, lse = run(dev, q, causal)
+    compare(o, lse, dt, host, q, causal)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_split_and_joined(dt):
+    """Lengths far apart: the long sequence is cut over many CTAs."""
+    rng = np.random.default_rng(5)
+    lens = (9000, 3, 130, 0, 2500)
+    dev, host = on_gpu(numpy_cache(rng, 5, 2, 16, 64, 64, lens), dt)
+    q = torch.tensor(rng.standard_normal((5, 8, 1, 64)), device="cuda").to(DT[dt])
+    o, lse = run(dev, q)
+    compare(o, lse, dt, host, q)
+    again = run(dev, q)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_large_scores(dt):
+    """Scores of several hundred, of both signs of the scale, and a zero scale."""
+    rng = np.random.default_rng(6)
+    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (400, 90)), dt)
+    q = torch.tensor(20 * rng.standard_normal((2, 4, 2, 64)), device="cuda").to(DT[dt])
+    for scale in (1.0, -1.0, 0.0):
+        o, lse = run(dev, q, scale=scale)
+        compare(o, lse, dt, host, q, scale=scale)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 4])
+def test_ragged_queries_leave_other_rows(dt, n):
+    rng = np.random.default_rng(7)
+    lens, q_len = (70, 0, 200, 129, 3), (n, n, 0, max(1, n - 1), n)
+    dev, host = on_gpu(numpy_cache(rng, 5, 2, 8, 64, 64, lens), dt)
+    q = torch.tensor(rng.standard_normal((5, 6, n, 64)), device="cuda").to(DT[dt])
+    out = torch.full((5, 6, n, 64), 7.0, dtype=DT[dt], device="cuda")
+    lse = torch.full((5, 6, n), 7.0, device="cuda")
+    o, l = run(dev, q, q_len=q_len, out=out, lse=lse)
+    assert o.data_ptr() == out.data_ptr() and l.data_ptr() == lse.data_ptr()
+    live = compare(o, l, dt, host, q, q_len=q_len)
+    rest = torch.tensor(~live, device="cuda")
+    assert (o[rest] == 7).all() and (l[rest] == 7).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [8, 64])
+def test_unused_rows_have_no_influence(dt, page):
+    """NaN and infinities in every row that no token owns, free pages included,
+    and table entries past the last page that lead nowhere."""
+    rng = np.random.default_rng(8)
+    lens = (1, 65, 131, 0)
+    c = numpy_cache(rng, 4, 2, page, 64, 64, lens)
+    q = torch.tensor(rng.standard_normal((4, 4, 3, 64)), device="cuda").to(DT[dt])
+    dev, host = on_gpu(c, dt)
+    want = run(dev, q)
+    compare(*want, dt, host, q)
+    used = np.zeros(c["k_pages"].shape[:1] + (page,), dtype=bool)
+    for b, L in enumerate(lens):
+        t = np.arange(L)
+        used[c["table"][b, t // page], t % page] = True
+        c["table"][b, -(-L // page):] = rng.integers(-2 ** 31, 2 ** 31 - 1, size=c["table"].shape[1] + L // -page)
+    for pool, bad in (("k_pages", np.nan), ("v_pages", np.inf)):
+        c[pool].transpose(0, 2, 1, 3)[~used] = bad
+    c["v_pages"].transpose(0, 2, 1, 3)[~used] = np.where(rng.random(c["v_pages"].transpose(0, 2, 1, 3)[~used].shape) < 0.5,
+                                                         np.nan, -np.inf)
+    dev, _ = on_gpu(c, dt)
+    got = run(dev, q)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_bad_page_numbers_and_lengths(dt):
+    """Page numbers outside the pool mask their tokens; lengths are clamped."""
+    rng = np.random.default_rng(10)
+    c = numpy_cache(rng, 3, 2, 16, 64, 64, (100, 100, 100), M=7)
+    P = c["ref"].shape[0]
+    c["table"][0, :7] = [c["table"][0, 0], -1, P, 2 ** 31 - 1, -2 ** 31, c["table"][0, 5], c["table"][0, 6]]
+    c["table"][1, :7] = -1                                 # nothing left: an empty row
+    c["lens"] = np.array([100, 100, -5], dtype=np.int32)
+    dev, host = on_gpu(c, dt)
+    q = torch.tensor(rng.standard_normal((3, 4, 2, 64)), device="cuda").to(DT[dt])
+    compare(*run(dev, q), dt, host, q)
+    c["lens"] = np.array([2 ** 31 - 1, 5, 1000], dtype=np.int32)     # the row holds 112
+    c["table"][2, 6] = 0
+    dev, host = on_gpu(c, dt)
+    compare(*run(dev, q), dt, host, dict(q=q)["q"])
+
+
+def test_pages_past_32_bits():
+    """A pool of more than 2^32 bytes per half, pages at both ends of it."""
+    P, Hkv, page, d = 20000, 8, 128, 128                    # 2.6e9 elements per pool
+    k = torch.empty(P, Hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    picks = [P - 1, 0, P - 2, P // 2, 16384, 16383]
+    for p in picks:
+        k[p] = torch.randn(Hkv, page, d, device="cuda", generator=g).to(k.dtype)
+        v[p] = torch.randn(Hkv, page, d, device="cuda", generator=g).to(k.dtype)
+    q = torch.randn(2, 16, 1, d, device="cuda", generator=g).to(k.dtype)
+    lens = torch.tensor([300, 290], dtype=torch.int32, device="cuda")
+    o, lse = lib.attn_decode(q, k, v, torch.tensor([picks[:3], picks[3:]], dtype=torch.int32, device="cuda"), lens)
+    ks, vs = k[picks].clone(), v[picks].clone()
+    small = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32, device="cuda")
+    o2, lse2 = lib.attn_decode(q, ks, vs, small, lens)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    host = dict(k_pages=ks.double().cpu().numpy(), v_pages=vs.double().cpu().numpy(),
+                table=small.cpu().numpy(), lens=lens.cpu().numpy())
+    compare(o, lse, "bf16", host, q)
+
+
+def test_many_sequences():
+    """More sequences than threads of a block, most of them short or idle."""
+    rng = np.random.default_rng(11)
+    B = 700
+    lens = rng.integers(0, 20, size=B)
+    lens[[3, 500]] = (900, 1500)
+    q_len = rng.integers(0, 2, size=B)
+    dev, host = on_gpu(numpy_cache(rng, B, 1, 8, 64, 64, lens), "bf16")
+    q = torch.tensor(rng.standard_normal((B, 2, 1, 64)), device="cuda").to(torch.bfloat16)
+    out = torch.zeros(B, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = run(dev, q, q_len=q_len, out=out)
+    compare(o, lse, "bf16", host, q, q_len=q_len)
+    assert (run(dev, q, q_len=np.zeros(B, dtype=np.int32), out=out.clone().fill_(3))[0] == 3).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_captured_streams_and_workspaces(dt):
+    """A captured call replayed on new inputs in place; calls at once on two
+    streams with workspaces of their own; a workspace of any contents."""
+    rng = np.random.default_rng(12)
+    lens = (700, 20)
+    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, lens), dt)
+    qs = [torch.tensor(rng.standard_normal((2, 4, 1, 64)), device="cuda").to(DT[dt]) for _ in range(2)]
+    want = [run(dev, q) for q in qs]
+    need = lib.attn_decode_workspace_size(2, 4, 2, 1, 64, 64, DT[dt])
+    ws = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"], workspace=w, stream=s)
+           for q, w, s in zip(qs, ws, streams) for _ in range(3)]
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i // 3][0]) and torch.equal(l, want[i // 3][1])
+    q = qs[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, l = lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"])
+    for i in (1, 0):
+        q.copy_(qs[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
+def test_refusals():
+    rng = np.random.default_rng(13)
+    dev, _ = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (20, 30)), "bf16")
+    q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    args = (dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"])
+    for bad in (q[:1], q.float(), q[..., :32].contiguous(), q.cpu(), q.transpose(1, 2)):
+        with pytest.raises((ValueError, TypeError, lib.AttnError)):
+            lib.attn_decode(bad, *args)
+    with pytest.raises(TypeError):
+        lib.attn_decode(q.half(), dev["k_pages"].half(), dev["v_pages"].half(), *args[2:])
+    with pytest.raises(ValueError):
+        lib.attn_decode(q, *args[:2], dev["table"].long(), dev["lens"])
+    with pytest.raises(ValueError):
+        lib.attn_decode(q, *args[:3], dev["lens"][:1])
+    with pytest.raises(ValueError):
+        lib.attn_decode(q, *args, q_len=torch.ones(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        lib.attn_decode(q, *args, out=torch.empty(2, 4, 1, 32, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(lib.AttnError) as e:
+        lib.attn_decode(torch.zeros(2, 5, 1, 64, dtype=torch.bfloat16, device="cuda"), *args)
+    assert e.value.code == 2
+    with pytest.raises(lib.AttnError) as e:
+        lib.attn_decode(q, *args, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 6
+    with pytest.raises(lib.AttnError) as e:
+        lib.attn_decode(q, *args, out=q)
+    assert e.value.code == 9
