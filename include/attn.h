@@ -247,7 +247,8 @@ typedef enum {
     ATTN_KERNEL_DECODE_SIMT = 13, /* CUDA-core decode over a paged cache       */
     ATTN_KERNEL_DECODE_JOIN = 14, /* joins the pieces of split decode items    */
     ATTN_KERNEL_CACHE_BOOKS = 15, /* table, lengths and counts of a cache call */
-    ATTN_KERNEL_CACHE_ROWS = 16   /* the rows that a cache call writes or moves */
+    ATTN_KERNEL_CACHE_ROWS = 16,  /* the rows that a cache call writes or moves */
+    ATTN_KERNEL_DECODE_TENSOR = 17 /* tensor-core decode over a paged cache    */
 } attn_kernel_id_t;
 
 typedef struct {

@@ -23,7 +23,7 @@
 #include "gemm_tc.cuh"
 #include "proj.cuh"
 #include "f32x_tc.cuh"
-#include "decode.cuh"
+#include "decode_tc.cuh"
 #include "cache.cuh"
 
 namespace {

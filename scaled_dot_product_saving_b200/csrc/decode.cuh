@@ -20,7 +20,7 @@
 namespace attn {
 namespace paged {
 
-constexpr int kRows = 16;             // query rows per item
+constexpr int kRows = 16;             // query rows per item on the CUDA cores
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxWidth = 128;
 
@@ -134,7 +134,11 @@ decode_simt(DecodeArgs a, const T* __restrict__ Q, const T* __restrict__ Kp, con
                 for (int r = 0; r < kRows; ++r) {
                     if (r < rows) {
                         float s = acc[r] * Cs[r];
-                        for (int j = 0; j < kTileKeys; ++j) s = fmaf(Ps[r * kTileKeys + j], Vs[j * dv + tid], s);
+                        for (int j = 0; j < kTileKeys; ++j) {
+                            // A token that this row does not see may hold anything.
+                            const float e = Ps[r * kTileKeys + j];
+                            if (e != 0.f) s = fmaf(e, Vs[j * dv + tid], s);
+                        }
                         acc[r] = s;
                     }
                 }
@@ -182,27 +186,28 @@ constexpr int kJoinThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts parts) {
+    grid_dependency_wait();
     const Head h = parts.head[blockIdx.x];
     if (h.b < 0) return;
-    const int hk = h.item / a.row_tiles, r0 = (h.item % a.row_tiles) * kRows;
+    const int hk = h.item / a.row_tiles, r0 = (h.item % a.row_tiles) * a.tile_rows;
     const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= min(kRows, a.rows - r0) || (r0 + r) % a.n >= h.nq) return;
+    if (r >= min(a.tile_rows, a.rows - r0) || (r0 + r) % a.n >= h.nq) return;
     const int first = blockIdx.x;
     float m = -INFINITY;
     for (int c = first + lane; c <= h.last; c += 32) {
         const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
-        m = fmaxf(m, parts.ml[(slot * kRows + r) * 2]);
+        m = fmaxf(m, parts.ml[(slot * a.tile_rows + r) * 2]);
     }
     m = simt::warp_max(m);
     const float ms = m == -INFINITY ? 0.f : m;
     float l = 0.f, acc[kMaxWidth / 32] = {};
     for (int c = first; c <= h.last; ++c) {
         const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
-        const float f = exp2f(parts.ml[(slot * kRows + r) * 2] - ms);
-        l = fmaf(parts.ml[(slot * kRows + r) * 2 + 1], f, l);
+        const float f = exp2f(parts.ml[(slot * a.tile_rows + r) * 2] - ms);
+        l = fmaf(parts.ml[(slot * a.tile_rows + r) * 2 + 1], f, l);
 #pragma unroll
         for (int k = 0; k < kMaxWidth / 32; ++k)
-            if (lane + 32 * k < a.dv) acc[k] = fmaf(parts.o[(slot * kRows + r) * a.dv + lane + 32 * k], f, acc[k]);
+            if (lane + 32 * k < a.dv) acc[k] = fmaf(parts.o[(slot * a.tile_rows + r) * a.dv + lane + 32 * k], f, acc[k]);
     }
     const size_t row = row_base(a, h.b, hk) + r0 + r;
     const float inv = l > 0.f ? 1.f / l : 0.f;

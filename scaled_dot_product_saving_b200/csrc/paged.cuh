@@ -79,7 +79,8 @@ struct DecodeArgs {
     const int* q_len;       // may be null: n queries everywhere
     int H, n, d, dv;
     int rows;               // query rows per key head: (H / Hkv) * n
-    int row_tiles;          // tiles of query rows per key head
+    int tile_rows;          // query rows per item
+    int row_tiles;          // items per key head
     int causal;
     float scale;
 };
@@ -177,8 +178,8 @@ struct Head {
     int nq;
 };
 struct Parts {
-    float* o;               // [2G][row tile][dv], not divided by l
-    float* ml;              // [2G][row tile][2]: maximum (base 2) and sum
+    float* o;               // [2G][tile_rows][dv], not divided by l
+    float* ml;              // [2G][tile_rows][2]: maximum (base 2) and sum
     Head* head;             // [G]
 };
 

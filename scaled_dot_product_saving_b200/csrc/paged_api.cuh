@@ -7,7 +7,9 @@ namespace {
 
 namespace pg = attn::paged;
 
-constexpr int kDecodeCtas = 444;        // most CTAs of a decode call (workspace slots)
+// Most CTAs of a decode call, and most CTAs times query rows of an item (64 rows
+// on one CTA an SM; 16 rows on two): what the workspace has slots for.
+constexpr int kDecodeCtas = 2 * 148, kDecodeRows = 64 * 148;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -64,7 +66,7 @@ struct DecodeWorkspace {
 };
 DecodeWorkspace carve_decode(int dv) {
     DecodeWorkspace w;
-    const size_t rows = 2ull * kDecodeCtas * pg::kRows;
+    const size_t rows = 2ull * kDecodeRows;
     w.o_off = 0;
     w.ml_off = round_up(rows * dv * sizeof(float), 256);
     w.head_off = w.ml_off + round_up(rows * 2 * sizeof(float), 256);
@@ -97,12 +99,58 @@ attn_status_t decode_simt(const pg::DecodeArgs& a, const void* Q, const void* Kp
 template <typename T>
 attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg::Parts& parts, int grid,
                           cudaStream_t st) {
-    const int rows = std::min(a.rows, pg::kRows);
-    const dim3 blocks(grid, (rows + pg::kJoinThreads / 32 - 1) / (pg::kJoinThreads / 32));
+    // A programmatic dependent of the decode kernel: its launch overlaps it. Not
+    // while tracing, which would count the overlap in this kernel's time.
+    cudaLaunchConfig_t cfg = {};
+    constexpr int kWarps = pg::kJoinThreads / 32;
+    cfg.gridDim = dim3(grid, (std::min(a.rows, a.tile_rows) + kWarps - 1) / kWarps);
+    cfg.blockDim = dim3(pg::kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_trace.on ? 0 : 1;
     return traced(ATTN_KERNEL_DECODE_JOIN, st, [&] {
-        pg::decode_join<T><<<blocks, pg::kJoinThreads, 0, st>>>(a, static_cast<T*>(O), LSE, parts);
+        if (cudaLaunchKernelEx(&cfg, pg::decode_join<T>, a, static_cast<T*>(O), LSE, parts) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return ATTN_ERR_CUDA;
+        }
         return launched();
     });
+}
+
+template <int DK, int DV, int R>
+attn_status_t decode_tc(const pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
+                        const pg::Parts& parts, int* grid, cudaStream_t st) {
+    using C = pg::DecodeCfg<DK, DV, R>;
+    CUtensorMap mk, mv;
+    const int page = 1 << a.g.page_log2, heads = a.g.P * a.g.Hkv, box = std::min(page, pg::kTileKeys);
+    if (!make_map_typed(&mk, Kp, a.d, page, heads, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, box) ||
+        !make_map_typed(&mv, Vp, a.dv, page, heads, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, box))
+        return ATTN_ERR_CUDA;
+    auto kern = pg::decode_tc<DK, DV, R>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    *grid = std::min(C::kCtasPerSm * sm_count(), std::min(kDecodeCtas, kDecodeRows / (16 * R)));
+    return traced(ATTN_KERNEL_DECODE_TENSOR, st, [&] {
+        kern<<<*grid, C::kThreads, C::kSmemBytes, st>>>(mk, mv, a, static_cast<const __nv_bfloat16*>(Q),
+                                                        static_cast<__nv_bfloat16*>(O), LSE, parts, kWaitBudgetNs);
+        return launched();
+    });
+}
+
+// Query rows of an item: as many of a key head's as there are, up to 64, since
+// every item reads its keys again.
+template <int DK, int DV>
+attn_status_t decode_tc_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
+                             const pg::Parts& parts, int* grid, cudaStream_t st) {
+    const int r = a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4;
+    a.tile_rows = 16 * r;
+    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
+    if (r == 1) return decode_tc<DK, DV, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    if (r == 2) return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    return decode_tc<DK, DV, 4>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
 }
 
 // ------------------------------------------------------------------- books
@@ -193,8 +241,11 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     if (!workspace || workspace_bytes < w.total) return ATTN_ERR_WORKSPACE;
     if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
 
-    pg::DecodeArgs a{g, table, lens, q_len, H, n, d, dv, H / Hkv * n, 0, causal != 0, scale};
-    a.row_tiles = (a.rows + pg::kRows - 1) / pg::kRows;
+    // bf16 runs on the tensor cores, fp32 on the CUDA cores; attn_set_path holds here too.
+    const bool tensor = dtype == ATTN_BF16 && g_path != ATTN_PATH_SIMT;
+    if (g_path == ATTN_PATH_TENSOR && !tensor) return ATTN_ERR_UNSUPPORTED;
+    pg::DecodeArgs a{g, table, lens, q_len, H, n, d, dv, H / Hkv * n, pg::kRows, 0, causal != 0, scale};
+    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     // The kernel numbers its units (key tiles of all items) times CTAs in 64 bits.
     if (static_cast<double>(B) * Hkv * a.row_tiles * ((static_cast<double>(max_pages) * page) / pg::kTileKeys + 1) >=
         9007199254740992.0)
@@ -210,14 +261,19 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const pg::Parts parts{reinterpret_cast<float*>(ws + w.o_off), reinterpret_cast<float*>(ws + w.ml_off),
                           reinterpret_cast<pg::Head*>(ws + w.head_off)};
-    const int grid = std::min(2 * sm_count(), kDecodeCtas);
-    if (dtype == ATTN_F32) {
+    int grid = std::min(2 * sm_count(), kDecodeCtas);
+    if (tensor)
+        s = d <= 64 ? (dv <= 64 ? decode_tc_rows<64, 64>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st)
+                                : decode_tc_rows<64, 128>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st))
+                    : (dv <= 64 ? decode_tc_rows<128, 64>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st)
+                                : decode_tc_rows<128, 128>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st));
+    else if (dtype == ATTN_F32)
         s = decode_simt<float>(a, Q, K_pages, V_pages, O, LSE, parts, grid, st);
-        if (s == ATTN_OK) s = decode_join<float>(a, O, LSE, parts, grid, st);
-    } else {
+    else
         s = decode_simt<__nv_bfloat16>(a, Q, K_pages, V_pages, O, LSE, parts, grid, st);
-        if (s == ATTN_OK) s = decode_join<__nv_bfloat16>(a, O, LSE, parts, grid, st);
-    }
+    if (s == ATTN_OK)
+        s = dtype == ATTN_F32 ? decode_join<float>(a, O, LSE, parts, grid, st)
+                              : decode_join<__nv_bfloat16>(a, O, LSE, parts, grid, st);
     if (s == ATTN_OK) g_last_launches = 2;
     return s;
 }

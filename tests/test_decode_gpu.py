@@ -72,6 +72,9 @@ CASES = [
     ((150, 90), 6, 3, 2, 40, 72, 16, True, "bf16"),                  # odd widths
     ((150, 90), 6, 3, 1, 8, 128, 8, True, "bf16"),
     ((150, 90), 2, 1, 3, 96, 16, 32, True, "bf16"),
+    ((150, 0, 70), 72, 1, 1, 128, 128, 16, True, "bf16"),            # more rows than one item takes
+    ((150, 3, 70), 30, 2, 5, 64, 128, 16, True, "bf16"),             # 75 rows, the last item nearly empty
+    ((150, 3, 70), 26, 2, 4, 128, 64, 32, True, "bf16"),
     ((1,), 2, 1, 1, 64, 64, 16, True, "f32"),
     ((0, 1, 63, 64, 65, 129), 8, 2, 1, 128, 128, 16, True, "f32"),
     ((700, 129), 20, 4, 1, 64, 64, 16, True, "f32"),
@@ -157,6 +160,34 @@ def test_unused_rows_have_no_influence(dt, page):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [2, 12])
+def test_later_tokens_of_a_draft_have_no_influence(dt, H):
+    """An infinite or NaN key or value of a draft's last tokens reaches the
+    queries that see it and no other."""
+    rng = np.random.default_rng(9)
+    lens, n = (64, 70, 8), 5
+    c = numpy_cache(rng, 3, 1, 16, 64, 64, lens)
+    q = torch.tensor(rng.standard_normal((3, H, n, 64)), device="cuda").to(DT[dt])
+    dev, host = on_gpu(c, dt)
+    want = run(dev, q)
+    compare(*want, dt, host, q)
+    for pool, bad in (("v_pages", np.nan), ("v_pages", np.inf), ("k_pages", np.nan)):
+        dirty = {k: v.copy() for k, v in c.items()}
+        for b, L in enumerate(lens):
+            t = L - 2                                       # seen by the last two queries
+            dirty[pool][c["table"][b, t // 16], 0, t % 16, 7] = bad
+        o, lse = run(on_gpu(dirty, dt)[0], q)
+        assert torch.equal(lse[..., :3], want[1][..., :3])
+        # the weights meet the finite values by another route: same sums to rounding
+        assert (o[..., :3, :].float() - want[0][..., :3, :].float()).abs().max() <= 2.0 ** -7 * want[0].float().abs().max()
+        reached = o[..., 3:, 7] if pool == "v_pages" else lse[..., 3:]
+        assert not torch.isfinite(reached).any()
+        if pool == "v_pages":
+            rest = [x for x in range(64) if x != 7]
+            assert torch.isfinite(o[..., rest]).all() and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_bad_page_numbers_and_lengths(dt):
     """Page numbers outside the pool mask their tokens; lengths are clamped."""
     rng = np.random.default_rng(10)
@@ -238,6 +269,27 @@ def test_captured_streams_and_workspaces(dt):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
+def test_paths():
+    """attn_set_path holds for attn_decode: the CUDA-core path for both types,
+    the tensor-core path for bf16 alone."""
+    rng = np.random.default_rng(14)
+    for dt in ("bf16", "f32"):
+        dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (200, 30)), dt)
+        q = torch.tensor(rng.standard_normal((2, 8, 2, 64)), device="cuda").to(DT[dt])
+        try:
+            lib.attn_set_path(lib.ATTN_PATH_SIMT)
+            compare(*run(dev, q), dt, host, q)
+            lib.attn_set_path(lib.ATTN_PATH_TENSOR)
+            if dt == "bf16":
+                compare(*run(dev, q), dt, host, q)
+            else:
+                with pytest.raises(lib.AttnError) as e:
+                    run(dev, q)
+                assert e.value.code == 4
+        finally:
+            lib.attn_set_path(lib.ATTN_PATH_AUTO)
 
 
 def test_refusals():
