@@ -364,68 +364,79 @@ def attn_outproj_bwd(o, wo, g, workspace=None, do=None, dwo=None, stream=None):
 
 
 # ------------------------------------------------------ paged key-value cache
-def _out(t, name, shape, dtype, device):
-    """An output the caller passed, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape)
-            or t.device != device or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t
+# These calls serve single tokens, where a step is a few microseconds: the
+# checks below are written for few operations per argument.
+_i32, _f32, _u8 = torch.int32, torch.float32, torch.uint8
 
 
-def _ints(t, name, shape, device):
-    """An int32 argument on the pools' device (None stays None)."""
-    return None if t is None else _out(t, name, shape, torch.int32, device)
+def _bad(name, shape, dtype, dev):
+    return ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
 
 
-def _opt(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(None if t is None else t.data_ptr())
+def _arg(t, name, shape, dtype, dev) -> int:
+    """The address of a tensor argument, checked."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except (AttributeError, RuntimeError):
+        pass
+    raise _bad(name, shape, dtype, dev)
 
 
-def _bytes(workspace, need, device):
-    if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    if not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+def _opt(t, name, shape, dtype, dev):
+    return None if t is None else _arg(t, name, shape, dtype, dev)
 
 
-def _pools(k_pages, v_pages, table, lens):
-    """(P, Hkv, page, d, dv, B, M) of a cache, its tensors checked."""
+def _pools(k_pages, v_pages, table):
+    """Device index, dtype, library code, (P, Hkv, page, d, dv, B, M), pools' addresses."""
     _require(k_pages, v_pages)
-    if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
-        raise ValueError("K and V pages must be [P, Hkv, page, d] and [P, Hkv, page, dv] tensors")
-    if v_pages.device != k_pages.device:
-        raise ValueError("K and V pages must live on one device")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be an int32 [B, max_pages] tensor")
-    _ints(table, "table", table.shape, k_pages.device)
-    B, M = table.shape
-    if lens is None:
-        raise ValueError("lens must be an int32 [B] tensor")
-    _ints(lens, "lens", (B,), k_pages.device)
-    P, Hkv, page, d = k_pages.shape
-    return P, Hkv, page, d, v_pages.shape[3], B, M
+    try:
+        P, Hkv, page, d = k_pages.shape
+        dv = v_pages.shape[3]
+        B, M = table.shape
+    except (ValueError, IndexError, AttributeError):
+        raise ValueError("a cache is [P, Hkv, page, d] and [P, Hkv, page, dv] pages and an int32 "
+                         "[B, max_pages] table") from None
+    dev, dt = k_pages.get_device(), k_pages.dtype
+    return (dev, dt, dtype_code(dt), (P, Hkv, page, d, dv, B, M), k_pages.data_ptr(),
+            _arg(v_pages, "v_pages", (P, Hkv, page, dv), dt, dev))
 
 
 class _On:
     """The device of a call's tensors and the stream it runs on made current,
-    so that what the binding allocates belongs to that stream."""
+    so that what the binding allocates belongs to that stream. Gives the
+    stream's handle."""
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-        self._device = torch.cuda.device(device)
-        self._stream = torch.cuda.stream(stream)       # None: no change
+    def __init__(self, dev, stream):
+        self._held = []
+        if stream is not None:
+            if stream.device_index != dev:
+                raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{dev}")
+            self._held.append(torch.cuda.stream(stream))       # its device, too
+        elif torch.cuda.current_device() != dev:
+            self._held.append(torch.cuda.device(dev))
+        self._dev = dev
 
-    def __enter__(self):
-        self._device.__enter__()
-        self._stream.__enter__()
+    def __enter__(self) -> int:
+        for c in self._held:
+            c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self._dev)
 
     def __exit__(self, *e):
-        self._stream.__exit__(*e)
-        self._device.__exit__(*e)
+        for c in reversed(self._held):
+            c.__exit__(*e)
+
+
+def _new(t, shape, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=_u8, device=dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace
 
 
 def attn_decode_workspace_size(B, H, Hkv, n, d, dv, dtype) -> int:
@@ -446,24 +457,24 @@ def attn_decode(q, k_pages, v_pages, table, lens, causal=True, scale=None, q_len
     query i of c is token lens[b] - c + i and sees the tokens up to itself.
     q_len (optional int32 [B]): queries of each sequence; rows past it are left
     as they were (undefined in an `out` that this call allocates)."""
-    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
-    _require(k_pages, q)
-    dev = k_pages.device
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d or q.device != dev:
-        raise ValueError(f"q must be a [{B}, H, n, {d}] tensor on {dev}")
+    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
+    if q.dim() != 4:
+        raise ValueError("q must be a [B, H, n, d] tensor")
     H, n = q.shape[1], q.shape[2]
-    q_len = _ints(q_len, "q_len", (B,), dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    code = dtype_code(q.dtype)
-    with _On(dev, stream):
-        out = _out(out, "out", (B, H, n, dvw), q.dtype, dev)
-        lse = _out(lse, "lse", (B, H, n), torch.float32, dev)
-        workspace = _bytes(workspace, attn_decode_workspace_size(B, H, Hkv, n, d, dvw, code), dev)
-        _check(lib.attn_decode(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens),
-                               _opt(q_len), _ptr(out), _ptr(lse), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), B, H, Hkv, n, d, dvw, P,
-                               page, M, code, int(bool(causal)), scale, _stream_handle(None)),
-               "attn_decode")
+    scale = 1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale)
+    with _On(dev, stream) as st:
+        out = _new(out, (B, H, n, dvw), dt, dev)
+        lse = _new(lse, (B, H, n), _f32, dev)
+        if workspace is None:
+            workspace = _scratch(None, attn_decode_workspace_size(B, H, Hkv, n, d, dvw, code), dev)
+        ws = _scratch(workspace, 0, dev)
+        status = lib.attn_decode(
+            _arg(q, "q", (B, H, n, d), dt, dev), kp, vp, _arg(table, "table", (B, M), _i32, dev),
+            _arg(lens, "lens", (B,), _i32, dev), _opt(q_len, "q_len", (B,), _i32, dev),
+            _arg(out, "out", (B, H, n, dvw), dt, dev), _arg(lse, "lse", (B, H, n), _f32, dev),
+            ws.data_ptr(), ws.nbytes, B, H, Hkv, n, d, dvw, P, page, M, code, 1 if causal else 0, scale, st)
+    if status != ATTN_OK:
+        raise AttnError(status, "attn_decode")
     return out, lse
 
 
@@ -473,29 +484,25 @@ def attn_cache_append(k, v, k_pages, v_pages, table, lens, ref, new_len=None, ta
     (table, lens, ref, info) after it. Pass table_out=table and so on to work
     in place. new_len (optional int32 [B]): valid rows of each sequence.
     info [3]: status (0: done), free pages, pages taken."""
-    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
-    _require(k_pages, k, v)
-    dev = k_pages.device
-    n = k.shape[2] if k.dim() == 4 else 0
-    if (tuple(k.shape) != (B, Hkv, n, d) or tuple(v.shape) != (B, Hkv, n, dvw) or k.device != dev
-            or v.device != dev):
-        raise ValueError(f"k, v must be [{B}, {Hkv}, n, {d}] and [{B}, {Hkv}, n, {dvw}] tensors on {dev}")
-    if ref is None:
-        raise ValueError("ref must be an int32 [P] tensor")
-    _ints(ref, "ref", (P,), dev)
-    new_len = _ints(new_len, "new_len", (B,), dev)
-    with _On(dev, stream):
-        table_out = _out(table_out, "table_out", (B, M), torch.int32, dev)
-        lens_out = _out(lens_out, "lens_out", (B,), torch.int32, dev)
-        ref_out = _out(ref_out, "ref_out", (P,), torch.int32, dev)
-        info = _out(info, "info", (3,), torch.int32, dev)
-        workspace = _bytes(workspace, attn_cache_workspace_size(B, M, P), dev)
-        _check(lib.attn_cache_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(table),
-                                     _ptr(lens), _ptr(ref), _opt(new_len), _ptr(table_out),
-                                     _ptr(lens_out), _ptr(ref_out), _ptr(info), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), B, Hkv, n, d, dvw,
-                                     P, page, M, dtype_code(k.dtype), _stream_handle(None)),
-               "attn_cache_append")
+    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
+    if k.dim() != 4:
+        raise ValueError("k must be a [B, Hkv, n, d] tensor")
+    n = k.shape[2]
+    with _On(dev, stream) as st:
+        table_out, lens_out = _new(table_out, (B, M), _i32, dev), _new(lens_out, (B,), _i32, dev)
+        ref_out, info = _new(ref_out, (P,), _i32, dev), _new(info, (3,), _i32, dev)
+        if workspace is None:
+            workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
+        ws = _scratch(workspace, 0, dev)
+        status = lib.attn_cache_append(
+            _arg(k, "k", (B, Hkv, n, d), dt, dev), _arg(v, "v", (B, Hkv, n, dvw), dt, dev), kp, vp,
+            _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
+            _arg(ref, "ref", (P,), _i32, dev), _opt(new_len, "new_len", (B,), _i32, dev),
+            _arg(table_out, "table_out", (B, M), _i32, dev), _arg(lens_out, "lens_out", (B,), _i32, dev),
+            _arg(ref_out, "ref_out", (P,), _i32, dev), _arg(info, "info", (3,), _i32, dev),
+            ws.data_ptr(), ws.nbytes, B, Hkv, n, d, dvw, P, page, M, code, st)
+    if status != ATTN_OK:
+        raise AttnError(status, "attn_cache_append")
     return table_out, lens_out, ref_out, info
 
 
@@ -505,25 +512,22 @@ def attn_cache_fork(k_pages, v_pages, table, lens, ref, src, keep=None, table_ou
     src[b] (int32 [B]; outside [0, B): b ends); returns (table, lens, ref,
     info) after it. Forks, beam reordering, shared prefixes, roll-back and
     freeing. info [3]: status (0: done), free pages, pages copied."""
-    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
-    dev = k_pages.device
-    if ref is None or src is None:
-        raise ValueError("ref must be an int32 [P] tensor and src an int32 [B] tensor")
-    _ints(ref, "ref", (P,), dev)
-    _ints(src, "src", (B,), dev)
-    keep = _ints(keep, "keep", (B,), dev)
-    with _On(dev, stream):
-        table_out = _out(table_out, "table_out", (B, M), torch.int32, dev)
-        lens_out = _out(lens_out, "lens_out", (B,), torch.int32, dev)
-        ref_out = _out(ref_out, "ref_out", (P,), torch.int32, dev)
-        info = _out(info, "info", (3,), torch.int32, dev)
-        workspace = _bytes(workspace, attn_cache_workspace_size(B, M, P), dev)
-        _check(lib.attn_cache_fork(_ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens), _ptr(ref),
-                                   _ptr(src), _opt(keep), _ptr(table_out), _ptr(lens_out), _ptr(ref_out),
-                                   _ptr(info), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), B, Hkv, d, dvw, P, page,
-                                   M, dtype_code(k_pages.dtype), _stream_handle(None)),
-               "attn_cache_fork")
+    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
+    with _On(dev, stream) as st:
+        table_out, lens_out = _new(table_out, (B, M), _i32, dev), _new(lens_out, (B,), _i32, dev)
+        ref_out, info = _new(ref_out, (P,), _i32, dev), _new(info, (3,), _i32, dev)
+        if workspace is None:
+            workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
+        ws = _scratch(workspace, 0, dev)
+        status = lib.attn_cache_fork(
+            kp, vp, _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
+            _arg(ref, "ref", (P,), _i32, dev), _arg(src, "src", (B,), _i32, dev),
+            _opt(keep, "keep", (B,), _i32, dev), _arg(table_out, "table_out", (B, M), _i32, dev),
+            _arg(lens_out, "lens_out", (B,), _i32, dev), _arg(ref_out, "ref_out", (P,), _i32, dev),
+            _arg(info, "info", (3,), _i32, dev), ws.data_ptr(), ws.nbytes, B, Hkv, d, dvw, P, page, M,
+            code, st)
+    if status != ATTN_OK:
+        raise AttnError(status, "attn_cache_fork")
     return table_out, lens_out, ref_out, info
 
 
@@ -532,21 +536,19 @@ def attn_cache_compact(k_pages, v_pages, table, lens, ref, table_out=None, ref_o
     """The live pages to the front of the pools; returns (table, ref, remap,
     info) after it. remap [P]: the new number of each page, -1 if free.
     info [3]: 0, free pages, pages moved."""
-    P, Hkv, page, d, dvw, B, M = _pools(k_pages, v_pages, table, lens)
-    dev = k_pages.device
-    if ref is None:
-        raise ValueError("ref must be an int32 [P] tensor")
-    _ints(ref, "ref", (P,), dev)
-    with _On(dev, stream):
-        table_out = _out(table_out, "table_out", (B, M), torch.int32, dev)
-        ref_out = _out(ref_out, "ref_out", (P,), torch.int32, dev)
-        remap = _out(remap, "remap", (P,), torch.int32, dev)
-        info = _out(info, "info", (3,), torch.int32, dev)
-        workspace = _bytes(workspace, attn_cache_workspace_size(B, M, P), dev)
-        _check(lib.attn_cache_compact(_ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens), _ptr(ref),
-                                      _ptr(table_out), _ptr(ref_out), _ptr(remap), _ptr(info),
-                                      _ptr(workspace), workspace.numel() * workspace.element_size(), B,
-                                      Hkv, d, dvw, P, page, M, dtype_code(k_pages.dtype),
-                                      _stream_handle(None)),
-               "attn_cache_compact")
+    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
+    with _On(dev, stream) as st:
+        table_out, ref_out = _new(table_out, (B, M), _i32, dev), _new(ref_out, (P,), _i32, dev)
+        remap, info = _new(remap, (P,), _i32, dev), _new(info, (3,), _i32, dev)
+        if workspace is None:
+            workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
+        ws = _scratch(workspace, 0, dev)
+        status = lib.attn_cache_compact(
+            kp, vp, _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
+            _arg(ref, "ref", (P,), _i32, dev), _arg(table_out, "table_out", (B, M), _i32, dev),
+            _arg(ref_out, "ref_out", (P,), _i32, dev), _arg(remap, "remap", (P,), _i32, dev),
+            _arg(info, "info", (3,), _i32, dev), ws.data_ptr(), ws.nbytes, B, Hkv, d, dvw, P, page, M,
+            code, st)
+    if status != ATTN_OK:
+        raise AttnError(status, "attn_cache_compact")
     return table_out, ref_out, remap, info

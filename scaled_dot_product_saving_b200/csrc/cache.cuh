@@ -2,13 +2,18 @@
 // and the kernels that move its rows.
 //
 // A page is free when its reference count is zero (or, which no call makes,
-// less). Pages are handed out
-// lowest number first, so every result is a function of the inputs alone. The
-// three book-keeping kernels run as one cluster of kBookCtas CTAs: their
-// phases depend on one another through counts over all pages, and a cluster's
-// hardware barrier separates them without a launch per phase. They work from
-// device memory only, never through the host, and leave the list of rows to
-// move in the workspace for the copy kernel launched after them.
+// less). Pages are handed out lowest number first, so every result is a
+// function of the inputs alone. The three book-keeping kernels run as one
+// cluster of kBookCtas CTAs: their phases depend on one another through counts
+// over all pages, and a cluster's hardware barrier separates them without a
+// launch per phase. They work from device memory only, never through the
+// host, and leave the list of rows to move in the workspace for the copy
+// kernel launched after them.
+//
+// What bounds the books is latency: a phase is two or three dependent reads of
+// L2 and a barrier, about 2 us, whatever the sizes up to some ten thousand
+// pages. So a phase reads what it can at once, sums that can go together go
+// through one scan, and what a thread knows of its sequence stays in registers.
 //
 // A table, length array or count array may be written in place (output ==
 // input): every value that a phase overwrites has been read before the
@@ -18,20 +23,22 @@
 #include <cstdint>
 
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace attn {
 namespace paged {
 
-constexpr int kBookCtas = 1;
+constexpr int kBookCtas = 8;
 constexpr int kBookThreads = 1024;
 constexpr int kBookWarps = kBookThreads / 32;
+constexpr int kAllWarps = kBookCtas * kBookWarps, kAllThreads = kBookCtas * kBookThreads;
 constexpr int kNone = 0x7fffffff;
 
 // info[0]; the header documents the values.
 enum : int { kInfoOk = 0, kInfoNoPages = 1, kInfoTableFull = 2, kInfoSharedTail = 3 };
 
 struct Move {            // rows [0, rows) of every head of page src, to page dst
-    int src, dst, rows, pad;
+    int src, dst, rows, entry;   // fork: the table entry that gets dst
 };
 
 // Words of the control block at the start of the workspace.
@@ -48,11 +55,10 @@ struct Books {
     int* info;           // status, free pages, pages taken / copied / moved
     // workspace
     int* control;        // [kCtlWords]
-    int* first;          // [B + 1]
-    int* after;          // [B]
+    int* after;          // [B]  new length
     int* start;          // [B]  append: old length; fork: last page of the source, if partly filled
-    int* base;           // [P]
-    int* key;            // [P]
+    int* base;           // [P]  fork: references besides last pages; compact: holes
+    int* key;            // [P]  append: table entry of each page taken; fork: who keeps it; compact: pages to move
     int* stage;          // [B, M]
     Move* moves;         // [max(B, P)]
 };
@@ -72,41 +78,29 @@ __device__ __forceinline__ void cluster_sync() {
 // (CTA, warp), so that ranks follow page numbers.
 __device__ __forceinline__ void page_range(int P, int* lo, int* hi) {
     const long long w = (long long)cluster_rank() * kBookWarps + (threadIdx.x >> 5);
-    constexpr long long n = kBookCtas * kBookWarps;
-    *lo = int(P * w / n);
-    *hi = int(P * (w + 1) / n);
+    *lo = int(P * w / kAllWarps);
+    *hi = int(P * (w + 1) / kAllWarps);
 }
 
-// How many pages of the warp's range satisfy the predicate.
-template <typename F>
-__device__ __forceinline__ int count_pages(int lo, int hi, F&& pred) {
-    int c = 0;
-#pragma unroll 4
-    for (int p = lo + int(threadIdx.x & 31); p < hi; p += 32) c += pred(p) ? 1 : 0;
-    return __reduce_add_sync(0xffffffffu, c);
+// Two sums through one scan: pages (high word) counted per warp, and a count
+// per thread (low word). Both totals are below 2^31.
+__device__ __forceinline__ long long both(int pages, int count) {
+    return ((threadIdx.x & 31) == 0 ? (long long)pages << 32 : 0ll) + count;
 }
 
-// Rank of the warp's first hit among the hits of all CTAs: begin() before a
-// cluster_sync, end() after it.
-struct Ranker {
-    int warp_before;
-    __device__ void begin(int hits, int* scratch, int* sums) {
-        int total;
-        const int before = block_exclusive((threadIdx.x & 31) == 0 ? hits : 0, scratch, &total);
-        warp_before = __shfl_sync(0xffffffffu, before, 0);
-        if (threadIdx.x == 0) sums[cluster_rank()] = total;
+// The totals of all CTAs' pages, read after a cluster_sync: those of earlier
+// CTAs, and all.
+__device__ __forceinline__ int pages_before(const int* sums, int* total) {
+    int before = 0, all = 0;
+#pragma unroll
+    for (int c = 0; c < kBookCtas; ++c) {
+        const int s = __ldcg(sums + c);
+        if (c < int(cluster_rank())) before += s;
+        all += s;
     }
-    __device__ int end(const int* sums, int* total) const {
-        int before = 0, all = 0;
-        for (int c = 0; c < kBookCtas; ++c) {
-            const int s = sums[c];
-            if (c < int(cluster_rank())) before += s;
-            all += s;
-        }
-        *total = all;
-        return before + warp_before;
-    }
-};
+    *total = all;
+    return before;
+}
 
 // This thread's contiguous share of the sequences, over one CTA.
 __device__ __forceinline__ void thread_share(int B, int* b0, int* b1) {
@@ -115,30 +109,41 @@ __device__ __forceinline__ void thread_share(int B, int* b0, int* b1) {
     *b1 = min(B, *b0 + chunk);
 }
 
+// f(b, j0) for blocks of 128 entries [j0, j0 + 128) of every table row, a warp
+// each, over the cluster: four entries a lane keep loads in flight.
+constexpr int kRowBlock = 128;
+template <typename F>
+__device__ __forceinline__ void table_blocks(const Geometry& g, F&& f) {
+    const int blocks = (g.M + kRowBlock - 1) / kRowBlock;
+    const long long items = (long long)g.B * blocks;
+    for (long long x = (long long)cluster_rank() * kBookWarps + (threadIdx.x >> 5); x < items; x += kAllWarps) {
+        const int b = int(x / blocks);
+        f(b, int(x - (long long)b * blocks) * kRowBlock);
+    }
+}
+
 // ------------------------------------------------------------------- append
 __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const int* new_len, int n) {
-    __shared__ int scratch[33];
+    grid_launch_dependents();                       // the copy kernel may set up meanwhile
+    __shared__ long long scratch[33];
+    __shared__ int full_s, shared_s;
     const Geometry& g = k.g;
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = int(cluster_rank());
-    const int gwarp = rank * kBookWarps + (tid >> 5);
     const int page_mask = (1 << g.page_log2) - 1, room = g.M << g.page_log2;
+    const bool same_ref = k.ref_out == k.ref, same_table = k.table_out == k.table;
+    if (tid == 0) full_s = shared_s = 0;
 
-    // Free pages, and (first CTA) the pages that each sequence needs.
-    int lo, hi;
-    page_range(g.P, &lo, &hi);
-    Ranker ranker;
-    ranker.begin(count_pages(lo, hi, [&](int p) { return k.ref[p] <= 0; }), scratch, k.control + kCtlSums);
+    // (First CTA) the pages that each sequence needs.
+    int b0 = 0, b1 = 0, need = 0, full = 0, shared = 0, len = 0, add = 0;
     if (rank == 0) {
-        int b0, b1;
         thread_share(g.B, &b0, &b1);
-        int need = 0, full = 0, shared = 0;
         for (int b = b0; b < b1; ++b) {
-            const int len = clamp_len(k.lens[b], g);
-            const int add = new_len ? min(max(new_len[b], 0), n) : n;
+            len = clamp_len(k.lens[b], g);
+            add = new_len ? min(max(new_len[b], 0), n) : n;
             if (add > room - len) {
                 full = 1;
-                continue;
+                add = 0;                            // the call is refused as a whole below
             }
             if (add > 0 && (len & page_mask) != 0) {
                 // The page that goes on being filled must be this sequence's alone.
@@ -147,31 +152,69 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const i
             }
             need += pages_of(len + add, g.page_log2) - pages_of(len, g.page_log2);
         }
-        int total;
-        int before = block_exclusive(need, scratch, &total);
-        for (int b = b0; b < b1; ++b) {
-            const int len = clamp_len(k.lens[b], g);
-            int add = new_len ? min(max(new_len[b], 0), n) : n;
-            if (add > room - len) add = 0;          // the call is refused as a whole below
-            k.first[b] = before;
-            k.start[b] = len;
-            k.after[b] = len + add;
-            before += pages_of(len + add, g.page_log2) - pages_of(len, g.page_log2);
+    }
+    // Free pages; the counts are copied on the way. Lane i holds which pages of
+    // the warp's i-th block of 32 are free, for its first 1,024 pages.
+    int lo, hi, count = 0;
+    unsigned held = 0;
+    page_range(g.P, &lo, &hi);
+#pragma unroll 4
+    for (int p0 = lo, i = 0; p0 < hi; p0 += 32, ++i) {
+        const int p = p0 + lane;
+        const int r = p < hi ? k.ref[p] : 1;
+        if (!same_ref && p < hi) k.ref_out[p] = r;
+        const unsigned hits = __ballot_sync(0xffffffffu, r <= 0);
+        if (lane == i) held = hits;
+        count += __popc(hits);
+    }
+    if (!same_table) {
+        table_blocks(g, [&](int b, int j0) {
+#pragma unroll
+            for (int j = j0 + lane; j < j0 + kRowBlock; j += 32)
+                if (j < g.M) k.table_out[size_t(b) * g.M + j] = k.table[size_t(b) * g.M + j];
+        });
+    }
+    __syncthreads();                                // full_s, shared_s are zero
+    if (full) full_s = 1;
+    if (shared) shared_s = 1;
+    long long totals;
+    const long long before = block_exclusive(both(count, need), scratch, &totals);
+    if (tid == 0) k.control[kCtlSums + rank] = int(totals >> 32);
+    if (rank == 0) {
+        // Page q of the call goes to table entry key[q]; sequences in order.
+        int q0 = int(before & 0x7fffffff);
+        for (int b = b0; __any_sync(0xffffffffu, b < b1); ++b) {
+            if (b < b1 && b1 - b0 > 1) {            // else it is in registers still
+                len = clamp_len(k.lens[b], g);
+                add = new_len ? min(max(new_len[b], 0), n) : n;
+                if (add > room - len) add = 0;
+            }
+            int mine = 0, at = 0;
+            if (b < b1) {
+                k.start[b] = len;
+                k.after[b] = len + add;
+                at = pages_of(len, g.page_log2);
+                mine = pages_of(len + add, g.page_log2) - at;
+            }
+            for (unsigned some = __ballot_sync(0xffffffffu, mine > 0); some; some &= some - 1) {
+                const int l = __ffs(some) - 1;
+                const int c = __shfl_sync(0xffffffffu, mine, l), q = __shfl_sync(0xffffffffu, q0, l);
+                const int e = __shfl_sync(0xffffffffu, b * g.M + at, l);
+                for (int x = lane; x < min(c, g.P - q); x += 32) k.key[q + x] = e + x;
+            }
+            q0 += mine;
         }
-        full = __syncthreads_or(full);
-        shared = __syncthreads_or(shared);
         if (tid == 0) {
-            k.first[g.B] = total;
-            k.control[kCtlNeed] = total;
-            k.control[kCtlFlags] = shared ? kInfoSharedTail : full ? kInfoTableFull : kInfoOk;
+            k.control[kCtlNeed] = int(totals & 0x7fffffff);
+            k.control[kCtlFlags] = shared_s ? kInfoSharedTail : full_s ? kInfoTableFull : kInfoOk;
         }
     }
     cluster_sync();
 
     int total_free;
-    int at = ranker.end(k.control + kCtlSums, &total_free);
-    const int need = k.control[kCtlNeed];
-    int status = k.control[kCtlFlags];
+    int at = pages_before(k.control + kCtlSums, &total_free) + int(__shfl_sync(0xffffffffu, before, 0) >> 32);
+    need = __ldcg(k.control + kCtlNeed);
+    int status = __ldcg(k.control + kCtlFlags);
     if (status == kInfoOk && need > total_free) status = kInfoNoPages;
     const bool ok = status == kInfoOk;
     if (rank == 0 && tid == 0) {
@@ -180,67 +223,127 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const i
         k.info[2] = ok ? need : 0;
         k.control[kCtlMoves] = ok;                  // the copy kernel writes nothing otherwise
     }
-    // The free page of rank q goes to the sequence b with first[b] <= q < first[b + 1].
-    const bool same_ref = k.ref_out == k.ref;
-    for (int p0 = lo; p0 < hi; p0 += 32) {
-        if (same_ref && (!ok || at >= need)) break;
-        const int p = p0 + lane;
-        const int r = p < hi ? k.ref[p] : 1;
-        const unsigned hits = __ballot_sync(0xffffffffu, r <= 0);
-        const int q = at + __popc(hits & ((1u << lane) - 1u));
-        at += __popc(hits);
-        if (ok && r <= 0 && q < need) {
-            int b0 = 0, b1 = g.B;                   // last b with first[b] <= q
-            while (b1 - b0 > 1) {
-                const int mid = (b0 + b1) >> 1;
-                if (k.first[mid] <= q) b0 = mid;
-                else b1 = mid;
+    if (ok) {
+        for (int p0 = lo, i = 0; p0 < hi && at < need; p0 += 32, ++i) {
+            const int p = p0 + lane;
+            const unsigned hits = i < 32 ? __shfl_sync(0xffffffffu, held, i)
+                                         : __ballot_sync(0xffffffffu, p < hi && k.ref[p] <= 0);
+            const int q = at + __popc(hits & ((1u << lane) - 1u));
+            at += __popc(hits);
+            if ((hits >> lane & 1) && q < need) {
+                k.table_out[__ldcg(k.key + q)] = p;
+                k.ref_out[p] = 1;
             }
-            const int slot = pages_of(k.start[b0], g.page_log2) + (q - k.first[b0]);
-            k.table_out[size_t(b0) * g.M + slot] = p;
-            k.ref_out[p] = 1;
-        } else if (!same_ref && p < hi) {
-            k.ref_out[p] = r;
         }
     }
-    if (k.table_out != k.table) {
-        for (int b = gwarp; b < g.B; b += kBookCtas * kBookWarps) {
-            const int from = ok ? pages_of(k.start[b], g.page_log2) : 0;
-            const int to = ok ? pages_of(k.after[b], g.page_log2) : 0;
-            const size_t row = size_t(b) * g.M;
-            for (int j = lane; j < g.M; j += 32)
-                if (j < from || j >= to) k.table_out[row + j] = k.table[row + j];
+    if (rank == 0) {
+        for (int b = b0; b < b1; ++b) {
+            if (b1 - b0 > 1) add = k.after[b] - (len = k.start[b]);
+            if (ok) k.lens_out[b] = len + add;
+            else if (k.lens_out != k.lens) k.lens_out[b] = k.lens[b];
         }
     }
-    if (ok || k.lens_out != k.lens)
-        for (int b = rank * kBookThreads + tid; b < g.B; b += kBookCtas * kBookThreads)
-            k.lens_out[b] = ok ? k.after[b] : k.lens[b];
 }
 
-// New rows K [B, Hkv, n, wk], V [B, Hkv, n, wv] into their pages; widths in
-// 16-byte units. One thread per 16 bytes.
-constexpr int kCopyThreads = 256;
+// The copy kernels start while the books are still being written: what they
+// read of them they read from L2, after the wait.
+//
+// A warp takes kSpan 16-byte units at a time, four a lane in flight. The units
+// of one (sequence, head), or one head of a page to move, are its rows of K and
+// then its rows of V; widths wk, wv in units.
+constexpr int kCopyThreads = 256, kSpan = 128;
 
+// New rows K [B, Hkv, n, wk], V [B, Hkv, n, wv] into their pages.
 __global__ void __launch_bounds__(kCopyThreads)
 append_rows(Geometry g, const uint4* __restrict__ K, const uint4* __restrict__ V, uint4* __restrict__ Kp,
-            uint4* __restrict__ Vp, const int* __restrict__ table, const int* control, const int* start,
-            const int* after, int n, int wk, int wv) {
-    if (!control[kCtlMoves]) return;
-    const int w = wk + wv, page = 1 << g.page_log2;
-    const unsigned long long total = (unsigned long long)g.B * g.Hkv * n * w;
-    for (unsigned long long x = (unsigned long long)blockIdx.x * kCopyThreads + threadIdx.x; x < total;
-         x += (unsigned long long)gridDim.x * kCopyThreads) {
-        const unsigned long long row = x / w;
-        const int c = int(x - row * w);
-        const unsigned long long bh = row / n;
-        const int i = int(row - bh * n), b = int(bh / g.Hkv), h = int(bh - (unsigned long long)b * g.Hkv);
-        const int t = start[b] + i;
-        if (t >= after[b]) continue;
-        const int p = table[size_t(b) * g.M + (t >> g.page_log2)];
-        if (!page_ok(p, g.P)) continue;
-        const size_t dst = (size_t(p) * g.Hkv + h) * page + (t & (page - 1));
-        if (c < wk) Kp[dst * wk + c] = K[row * wk + c];
-        else Vp[dst * wv + c - wk] = V[row * wv + c - wk];
+            uint4* __restrict__ Vp, const int* table, const int* control, const int* start, const int* after,
+            int n, int wk, int wv) {
+    const int lane = threadIdx.x & 31, page = 1 << g.page_log2;
+    const unsigned long long units = (unsigned long long)n * (wk + wv), k_units = (unsigned long long)n * wk;
+    const unsigned long long spans = (units + kSpan - 1) / kSpan, items = spans * g.B * g.Hkv;
+    const unsigned long long stride = (unsigned long long)gridDim.x * (kCopyThreads / 32);
+    // With one span a warp, its rows are on the way before the books are read;
+    // with more, rows that turn out to be padding are not worth reading.
+    const bool early = items <= stride;
+    if (!early) {
+        grid_dependency_wait();
+        if (!__ldcg(control + kCtlMoves)) return;
+    }
+    for (unsigned long long x = (unsigned long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items;
+         x += stride) {
+        const unsigned long long bh = x / spans;
+        const unsigned long long u0 = (x - bh * spans) * kSpan + lane;
+        const int b = int(bh / g.Hkv), h = int(bh - (unsigned long long)b * g.Hkv);
+        int t0 = 0, add = n;
+        if (!early) {
+            t0 = __ldcg(start + b);
+            add = __ldcg(after + b) - t0;
+        }
+        uint4 v[4];
+        int i[4], c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned long long u = u0 + 32 * e;
+            i[e] = n;
+            if (u < k_units) {
+                i[e] = int(u / wk);
+                c[e] = int(u - (unsigned long long)i[e] * wk);
+                if (i[e] < add) v[e] = K[bh * k_units + u];
+            } else if (u < units) {
+                const unsigned long long y = u - k_units;
+                i[e] = int(y / wv);
+                c[e] = ~int(y - (unsigned long long)i[e] * wv);     // V's columns as complements
+                if (i[e] < add) v[e] = V[bh * (units - k_units) + y];
+            }
+        }
+        if (early) {
+            grid_dependency_wait();
+            if (!__ldcg(control + kCtlMoves)) return;
+            t0 = __ldcg(start + b);
+            add = __ldcg(after + b) - t0;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (i[e] >= add) continue;
+            const int t = t0 + i[e];
+            const int p = __ldcg(table + size_t(b) * g.M + (t >> g.page_log2));
+            if (!page_ok(p, g.P)) continue;
+            const size_t dst = (size_t(p) * g.Hkv + h) * page + (t & (page - 1));
+            if (c[e] >= 0) Kp[dst * wk + c[e]] = v[e];
+            else Vp[dst * wv + ~c[e]] = v[e];
+        }
+    }
+}
+
+// Rows [0, rows) of every head of the listed pages.
+__global__ void __launch_bounds__(kCopyThreads)
+move_rows(Geometry g, uint4* Kp, uint4* Vp, const int* control, const Move* moves, int wk, int wv) {
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const unsigned spans = ((unsigned(wk + wv) << g.page_log2) + kSpan - 1) / kSpan;
+    const unsigned long long items = (unsigned long long)__ldcg(control + kCtlMoves) * g.Hkv * spans;
+    const unsigned long long stride = (unsigned long long)gridDim.x * (kCopyThreads / 32);
+    for (unsigned long long x = (unsigned long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items;
+         x += stride) {
+        const unsigned long long qh = x / spans, q = qh / g.Hkv;
+        const unsigned u0 = unsigned(x - qh * spans) * kSpan + lane;
+        const int h = int(qh - q * g.Hkv);
+        const int4 m = __ldcg(reinterpret_cast<const int4*>(moves) + q);
+        const size_t from = (size_t(m.x) * g.Hkv + h) << g.page_log2, to = (size_t(m.y) * g.Hkv + h) << g.page_log2;
+        const unsigned k_units = unsigned(m.z) * wk, units = k_units + unsigned(m.z) * wv;
+        uint4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned u = u0 + 32 * e;
+            if (u < k_units) v[e] = Kp[from * wk + u];
+            else if (u < units) v[e] = Vp[from * wv + (u - k_units)];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned u = u0 + 32 * e;
+            if (u < k_units) Kp[to * wk + u] = v[e];
+            else if (u < units) Vp[to * wv + (u - k_units)] = v[e];
+        }
     }
 }
 
@@ -249,187 +352,232 @@ append_rows(Geometry g, const uint4* __restrict__ K, const uint4* __restrict__ V
 // shared, and a partly filled last page belongs to one sequence alone.
 //   base(p) = ref(p) - (uses in the old rows) + (full uses in the new rows)
 // counts who holds p besides its takers as a last page. With base(p) = 0 one
-// taker keeps p (the one it belonged to, else the lowest); every other taker
-// gets a copy in a fresh page.
+// taker keeps p (the one it belonged to, else the lowest: the least of `key`);
+// every other taker gets a copy in a fresh page.
 __global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int* src, const int* keep) {
-    __shared__ int scratch[33];
+    grid_launch_dependents();                       // the copy kernel may set up meanwhile
+    __shared__ long long scratch[33];
     const Geometry& g = k.g;
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = int(cluster_rank());
-    const int gwarp = rank * kBookWarps + (tid >> 5);
-    const int gthread = rank * kBookThreads + tid;
-    constexpr int kWarps = kBookCtas * kBookWarps, kThreads = kBookCtas * kBookThreads;
     const int page_mask = (1 << g.page_log2) - 1;
-    int lo, hi;
-    page_range(g.P, &lo, &hi);
+    const bool same_ref = k.ref_out == k.ref, same_table = k.table_out == k.table;
 
-    for (int p = gthread; p < g.P; p += kThreads) {
+    struct Seq {
+        int src, old_len, L;
+    };
+    auto seq = [&](int b) {
+        Seq q;
+        q.src = src[b];
+        q.old_len = clamp_len(k.lens[b], g);
+        const bool valid = q.src >= 0 && q.src < g.B;
+        q.L = valid ? clamp_len(k.lens[q.src], g) : 0;
+        if (valid && keep) q.L = min(max(keep[b], 0), q.L);
+        return q;
+    };
+
+    for (int p = rank * kBookThreads + tid; p < g.P; p += kAllThreads) {
         k.base[p] = k.ref[p];
         k.key[p] = kNone;
     }
+    // (First CTA) the last pages; a thread keeps its first sequence in registers.
+    int b0 = 0, b1 = 0;
+    if (rank == 0) thread_share(g.B, &b0, &b1);
+    Seq mine{-1, 0, 0};
+    int tail = -1;
+    for (int b = b0; b < b1; ++b) {
+        mine = seq(b);
+        tail = (mine.L & page_mask) != 0 ? k.table[size_t(mine.src) * g.M + (mine.L >> g.page_log2)] : -1;
+        k.start[b] = tail;
+        k.after[b] = mine.L;
+    }
+    const bool one = b1 - b0 <= 1;
     cluster_sync();
 
-    // Uses given up and taken. Pages that a sequence keeps in its own row cancel.
-    for (int b = gwarp; b < g.B; b += kWarps) {
-        const int len = clamp_len(k.lens[b], g), s = src[b];
-        const bool valid = s >= 0 && s < g.B;
-        int L = valid ? clamp_len(k.lens[s], g) : 0;
-        if (valid && keep) L = min(max(keep[b], 0), L);
-        const int had = pages_of(len, g.page_log2), full = L >> g.page_log2;
-        const int* mine = k.table + size_t(b) * g.M;
-        const int* from = k.table + size_t(valid ? s : b) * g.M;
-        for (int j = (s == b ? full : 0) + lane; j < had; j += 32) {
-            const int p = mine[j];
-            if (page_ok(p, g.P)) atomicSub(k.base + p, 1);
-        }
-        if (s != b) {
-            for (int j = lane; j < full; j += 32) {
+    // Uses given up and taken; pages that a sequence keeps in its own row
+    // cancel. Rows that come from elsewhere are staged: they may be overwritten.
+    table_blocks(g, [&](int b, int j0) {
+        const Seq q = seq(b);
+        const int had = pages_of(q.old_len, g.page_log2), full = q.L >> g.page_log2;
+        const bool home = q.src == b;
+        if (j0 >= max(had, full)) return;
+        const int* own = k.table + size_t(b) * g.M;
+        const int* from = k.table + size_t(full > 0 ? q.src : b) * g.M;
+#pragma unroll
+        for (int j = j0 + lane; j < j0 + kRowBlock; j += 32) {
+            if (j < had && !(home && j < full)) {
+                const int p = own[j];
+                if (page_ok(p, g.P)) atomicSub(k.base + p, 1);
+            }
+            if (j < full && !home) {
                 const int p = from[j];
                 if (page_ok(p, g.P)) atomicAdd(k.base + p, 1);
                 k.stage[size_t(b) * g.M + j] = p;
             }
         }
-        if (lane == 0) {
-            k.start[b] = (L & page_mask) != 0 ? from[full] : -1;
-            k.after[b] = L;
-        }
-    }
-    cluster_sync();
-
-    auto order_of = [&](int b) { return src[b] == b ? b : b + g.B; };
-    auto tail_of = [&](int b) {                        // a last page that can be followed, or -1
-        const int p = k.start[b];
-        return (k.after[b] & page_mask) != 0 && page_ok(p, g.P) ? p : -1;
+    });
+    // A last page that can be followed, or -1; its takers in order.
+    auto tail_of = [&](int b) {
+        const int p = one ? tail : k.start[b];
+        return ((one ? mine.L : k.after[b]) & page_mask) != 0 && page_ok(p, g.P) ? p : -1;
     };
-    for (int b = gthread; b < g.B; b += kThreads) {
+    auto order_of = [&](int b) { return (one ? mine.src : src[b]) == b ? b : b + g.B; };
+    for (int b = b0; b < b1; ++b) {
         const int p = tail_of(b);
-        if (p >= 0 && k.base[p] <= 0) atomicMin(k.key + p, order_of(b));
+        if (p >= 0) atomicMin(k.key + p, order_of(b));
     }
     cluster_sync();
 
-    // Who copies (in the order of sequences), and which pages are free.
+    // Who copies (in the order of sequences), and which pages are free: lane i
+    // holds those of the warp's i-th block of 32, for its first 1,024 pages.
     auto copies = [&](int b) {
         const int p = tail_of(b);
-        return p >= 0 && (k.base[p] > 0 || k.key[p] != order_of(b));
+        return p >= 0 && (__ldcg(k.base + p) > 0 || __ldcg(k.key + p) != order_of(b));
     };
-    Ranker ranker;
-    ranker.begin(count_pages(lo, hi, [&](int p) { return k.base[p] <= 0 && k.key[p] == kNone; }), scratch,
-                 k.control + kCtlSums);
+    int ncopy = 0;
+    for (int b = b0; b < b1; ++b) ncopy += copies(b) ? 1 : 0;
+    int lo, hi, count = 0;
+    unsigned held = 0;
+    page_range(g.P, &lo, &hi);
+    auto is_free = [&](int p) { return p < hi && __ldcg(k.base + p) <= 0 && __ldcg(k.key + p) == kNone; };
+#pragma unroll 4
+    for (int p0 = lo, i = 0; p0 < hi; p0 += 32, ++i) {
+        const unsigned hits = __ballot_sync(0xffffffffu, is_free(p0 + lane));
+        if (lane == i) held = hits;
+        count += __popc(hits);
+    }
+    long long totals;
+    const long long before = block_exclusive(both(count, ncopy), scratch, &totals);
+    if (tid == 0) k.control[kCtlSums + rank] = int(totals >> 32);
     if (rank == 0) {
-        int b0, b1;
-        thread_share(g.B, &b0, &b1);
-        int mine = 0, total;
-        for (int b = b0; b < b1; ++b) mine += copies(b) ? 1 : 0;
-        int at = block_exclusive(mine, scratch, &total);
+        int q = int(before & 0x7fffffff);
         for (int b = b0; b < b1; ++b) {
-            const bool c = copies(b);
-            k.first[b] = c ? at : -1;
-            if (c) {
-                k.moves[at].src = k.start[b];
-                k.moves[at].rows = k.after[b] & page_mask;
-                ++at;
-            }
+            const int L = one ? mine.L : k.after[b];
+            if ((L & page_mask) == 0) continue;
+            const bool c = one ? ncopy != 0 : copies(b);
+            const int entry = b * g.M + (L >> g.page_log2);
+            k.stage[entry] = c;                                  // staged entries end before it
+            if (c) k.moves[q++] = Move{one ? tail : k.start[b], -1, L & page_mask, entry};
         }
-        if (tid == 0) k.control[kCtlNeed] = total;
+        if (tid == 0) k.control[kCtlNeed] = int(totals & 0x7fffffff);
     }
     cluster_sync();
 
     int total_free;
-    int at = ranker.end(k.control + kCtlSums, &total_free);
-    const int need = k.control[kCtlNeed];
-    const bool ok = need <= total_free;
-    const bool same_ref = k.ref_out == k.ref;
-    int free_before = 0;                               // free pages of the counts as they came
-    for (int p0 = lo; p0 < hi; p0 += 32) {
+    int at = pages_before(k.control + kCtlSums, &total_free) + int(__shfl_sync(0xffffffffu, before, 0) >> 32);
+    const int need = __ldcg(k.control + kCtlNeed);
+    if (need > total_free) {
+        // Nothing changes; the free pages are those of the counts as they came.
+        int was_free = 0;
+        for (int p = lo + lane; p < hi; p += 32) {
+            const int r = k.ref[p];
+            was_free += r <= 0 ? 1 : 0;
+            if (!same_ref) k.ref_out[p] = r;
+        }
+        if (!same_table) {
+            table_blocks(g, [&](int b, int j0) {
+                for (int j = j0 + lane; j < min(g.M, j0 + kRowBlock); j += 32)
+                    k.table_out[size_t(b) * g.M + j] = k.table[size_t(b) * g.M + j];
+            });
+        }
+        if (k.lens_out != k.lens)
+            for (int b = b0; b < b1; ++b) k.lens_out[b] = k.lens[b];
+        long long sum;
+        (void)block_exclusive((long long)was_free, scratch, &sum);
+        if (tid == 0) k.control[kCtlFreed + rank] = int(sum);
+        cluster_sync();
+        if (rank == 0 && tid == 0) {
+            int now = 0;
+            for (int c = 0; c < kBookCtas; ++c) now += __ldcg(k.control + kCtlFreed + c);
+            k.info[0] = kInfoNoPages;
+            k.info[1] = now;
+            k.info[2] = 0;
+            k.control[kCtlMoves] = 0;
+        }
+        return;
+    }
+    if (rank == 0 && tid == 0) {
+        k.info[0] = kInfoOk;
+        k.info[1] = total_free - need;
+        k.info[2] = need;
+        k.control[kCtlMoves] = need;
+    }
+#pragma unroll 4
+    for (int p0 = lo, i = 0; p0 < hi; p0 += 32, ++i) {
         const int p = p0 + lane;
-        const int base = p < hi ? k.base[p] : 1, key = p < hi ? k.key[p] : kNone;
-        const bool free_page = base <= 0 && key == kNone;
-        const unsigned hits = __ballot_sync(0xffffffffu, free_page);
+        const unsigned hits = i < 32 ? __shfl_sync(0xffffffffu, held, i) : __ballot_sync(0xffffffffu, is_free(p));
         const int q = at + __popc(hits & ((1u << lane) - 1u));
         at += __popc(hits);
         if (p >= hi) continue;
-        if (ok) {
-            const bool taken = free_page && q < need;
-            if (taken) k.moves[q].dst = p;
-            k.ref_out[p] = taken ? 1 : max(base, 0) + (key != kNone ? 1 : 0);
+        if (hits >> lane & 1) {
+            if (q < need) {
+                k.moves[q].dst = p;
+                k.table_out[__ldcg(&k.moves[q].entry)] = p;
+            }
+            k.ref_out[p] = q < need ? 1 : 0;
         } else {
-            const int r = k.ref[p];
-            free_before += r <= 0 ? 1 : 0;
-            if (!same_ref) k.ref_out[p] = r;
+            const int held_by = __ldcg(k.base + p);
+            k.ref_out[p] = held_by > 0 ? held_by : 1;            // a last page that stays, if nobody else
         }
     }
-    if (!ok) {
-        int total;
-        (void)block_exclusive(free_before, scratch, &total);
-        if (tid == 0) k.control[kCtlFreed + rank] = total;
-    }
-    cluster_sync();
-    if (rank == 0 && tid == 0) {
-        int free_now = total_free - need;
-        if (!ok) {
-            free_now = 0;
-            for (int c = 0; c < kBookCtas; ++c) free_now += k.control[kCtlFreed + c];
-        }
-        k.info[0] = ok ? kInfoOk : kInfoNoPages;
-        k.info[1] = free_now;
-        k.info[2] = ok ? need : 0;
-        k.control[kCtlMoves] = ok ? need : 0;
-    }
-
-    const bool same_table = k.table_out == k.table;
-    for (int b = gwarp; b < g.B; b += kWarps) {
-        const size_t row = size_t(b) * g.M;
-        const int old_len = k.lens[b];
-        __syncwarp();
-        if (!ok) {
-            if (!same_table)
-                for (int j = lane; j < g.M; j += 32) k.table_out[row + j] = k.table[row + j];
-            if (lane == 0) k.lens_out[b] = old_len;
-            continue;
-        }
-        const int had = pages_of(clamp_len(old_len, g), g.page_log2);
-        const int L = k.after[b], full = L >> g.page_log2, has = pages_of(L, g.page_log2);
+    // The rows. In place, a sequence's own row only changes from its last page on.
+    table_blocks(g, [&](int b, int j0) {
+        const int L = __ldcg(k.after + b), had = pages_of(clamp_len(k.lens[b], g), g.page_log2);
+        const int full = L >> g.page_log2, has = pages_of(L, g.page_log2);
         const bool home = src[b] == b;
-        const int c = k.first[b];
-        const int last = c >= 0 ? k.moves[c].dst : k.start[b];
-        // In place, a sequence's own row only changes from its last page on.
-        const int end = same_table ? max(had, has) : g.M;
-        for (int j = (same_table && home ? full : 0) + lane; j < end; j += 32) {
+        const int last = __ldcg(k.start + b);
+        const bool copied = has > full && __ldcg(k.stage + size_t(b) * g.M + full);
+        const int from = same_table && home ? full : 0, end = same_table ? max(had, has) : g.M;
+        if (j0 + kRowBlock <= from || j0 >= end) return;
+        const size_t row = size_t(b) * g.M;
+#pragma unroll
+        for (int j = j0 + lane; j < j0 + kRowBlock; j += 32) {
+            if (j < from || j >= end || (copied && j == full)) continue;   // written with its page
             int p;
-            if (j < full) p = home ? k.table[row + j] : k.stage[row + j];
+            if (j < full) p = home ? k.table[row + j] : __ldcg(k.stage + row + j);
             else if (j < has) p = last;
             else p = j < had ? -1 : k.table[row + j];
             k.table_out[row + j] = p;
         }
-        if (lane == 0) k.lens_out[b] = L;
-    }
+    });
+    if (k.lens_out == k.lens) cluster_sync();                    // every row has read its old length
+    for (int b = b0; b < b1; ++b) k.lens_out[b] = one ? mine.L : k.after[b];
 }
 
 // ------------------------------------------------------------------ compact
 // L live pages. The k-th live page at or past L moves to the k-th free page
 // before L: the fewest moves, no page both read and written.
 __global__ void __launch_bounds__(kBookThreads, 1) compact_books(Books k, int* remap) {
-    __shared__ int scratch[33];
+    grid_launch_dependents();                       // the copy kernel may set up meanwhile
+    __shared__ long long scratch[33];
     const Geometry& g = k.g;
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = int(cluster_rank());
-    const int gwarp = rank * kBookWarps + (tid >> 5);
     const int gthread = rank * kBookThreads + tid;
-    constexpr int kThreads = kBookCtas * kBookThreads;
     int lo, hi;
     page_range(g.P, &lo, &hi);
     int* holes = k.base;
     int* high = k.key;
 
-    Ranker ranker;
-    ranker.begin(count_pages(lo, hi, [&](int p) { return k.ref[p] > 0; }), scratch, k.control + kCtlSums);
+    int count = 0;
+    unsigned held = 0;                              // live pages, as in append_books
+#pragma unroll 4
+    for (int p0 = lo, i = 0; p0 < hi; p0 += 32, ++i) {
+        const unsigned hits = __ballot_sync(0xffffffffu, p0 + lane < hi && k.ref[p0 + lane] > 0);
+        if (lane == i) held = hits;
+        count += __popc(hits);
+    }
+    long long totals;
+    const long long before = block_exclusive(both(count, 0), scratch, &totals);
+    if (tid == 0) k.control[kCtlSums + rank] = int(totals >> 32);
     cluster_sync();
     int live;
-    int at = ranker.end(k.control + kCtlSums, &live);
-    for (int p0 = lo; p0 < hi; p0 += 32) {
+    int at = pages_before(k.control + kCtlSums, &live) + int(__shfl_sync(0xffffffffu, before, 0) >> 32);
+    for (int p0 = lo, i = 0; p0 < hi; p0 += 32, ++i) {
         const int p = p0 + lane;
-        const bool is_live = p < hi && k.ref[p] > 0;
-        const unsigned hits = __ballot_sync(0xffffffffu, is_live);
+        const unsigned hits = i < 32 ? __shfl_sync(0xffffffffu, held, i)
+                                     : __ballot_sync(0xffffffffu, p < hi && k.ref[p] > 0);
+        const bool is_live = hits >> lane & 1;
         const int q = at + __popc(hits & ((1u << lane) - 1u));   // live pages before p
         at += __popc(hits);
         if (p >= hi) continue;
@@ -442,17 +590,18 @@ __global__ void __launch_bounds__(kBookThreads, 1) compact_books(Books k, int* r
     }
     if (gthread == 0 && live == g.P) k.control[kCtlNeed] = 0;
     cluster_sync();
-    const int m = k.control[kCtlNeed];
+    const int m = __ldcg(k.control + kCtlNeed);
     // A moved page's count goes to its hole. Counts of holes and of moved pages
     // are written by the second loop alone; the others stay.
     if (k.ref_out != k.ref) {
-        for (int p = gthread; p < g.P; p += kThreads) {
+#pragma unroll 4
+        for (int p = gthread; p < g.P; p += kAllThreads) {
             const int r = k.ref[p];
             if (r > 0 ? p < live : p >= live) k.ref_out[p] = r;
         }
     }
-    for (int q = gthread; q < m; q += kThreads) {
-        const int from = high[m - 1 - q], to = holes[q];
+    for (int q = gthread; q < m; q += kAllThreads) {
+        const int from = __ldcg(high + (m - 1 - q)), to = __ldcg(holes + q);
         remap[from] = to;
         k.ref_out[to] = k.ref[from];
         k.ref_out[from] = 0;
@@ -466,30 +615,27 @@ __global__ void __launch_bounds__(kBookThreads, 1) compact_books(Books k, int* r
     }
     cluster_sync();
     const bool same_table = k.table_out == k.table;
-    for (int b = gwarp; b < g.B; b += kBookCtas * kBookWarps) {
+    table_blocks(g, [&](int b, int j0) {
         const int had = pages_of(clamp_len(k.lens[b], g), g.page_log2);
+        const int end = same_table ? had : g.M;
         const size_t row = size_t(b) * g.M;
-        for (int j = lane; j < (same_table ? had : g.M); j += 32) {
-            const int p = k.table[row + j];
-            k.table_out[row + j] = j < had && page_ok(p, g.P) ? remap[p] : p;
+        int p[kRowBlock / 32];
+#pragma unroll
+        for (int e = 0; e < kRowBlock / 32; ++e) {
+            const int j = j0 + lane + 32 * e;
+            p[e] = j < end ? k.table[row + j] : -1;
         }
-    }
-}
-
-// Rows [0, rows) of every head of the listed pages, K then V; widths in
-// 16-byte units. One block per (move, head) at a time.
-__global__ void __launch_bounds__(kCopyThreads)
-move_rows(Geometry g, uint4* Kp, uint4* Vp, const int* control, const Move* moves, int wk, int wv) {
-    const unsigned long long items = (unsigned long long)control[kCtlMoves] * g.Hkv;
-    for (unsigned long long x = blockIdx.x; x < items; x += gridDim.x) {
-        const unsigned long long q = x / g.Hkv;
-        const int h = int(x - q * g.Hkv);
-        const Move mv = moves[q];
-        const size_t from = (size_t(mv.src) * g.Hkv + h) << g.page_log2;
-        const size_t to = (size_t(mv.dst) * g.Hkv + h) << g.page_log2;
-        for (int c = threadIdx.x; c < mv.rows * wk; c += kCopyThreads) Kp[to * wk + c] = Kp[from * wk + c];
-        for (int c = threadIdx.x; c < mv.rows * wv; c += kCopyThreads) Vp[to * wv + c] = Vp[from * wv + c];
-    }
+#pragma unroll
+        for (int e = 0; e < kRowBlock / 32; ++e) {
+            const int j = j0 + lane + 32 * e;
+            if (j < had && page_ok(p[e], g.P)) p[e] = __ldcg(remap + p[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kRowBlock / 32; ++e) {
+            const int j = j0 + lane + 32 * e;
+            if (j < end) k.table_out[row + j] = p[e];
+        }
+    });
 }
 
 }  // namespace paged

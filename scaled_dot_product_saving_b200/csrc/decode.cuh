@@ -61,6 +61,7 @@ decode_simt(DecodeArgs a, const T* __restrict__ Q, const T* __restrict__ Kp, con
     Walker w;
     w.start(a, scratch, found);
     if (tid == 0) parts.head[blockIdx.x].b = -1;
+    grid_launch_dependents();
     const float scale_log2 = a.scale * 1.4426950408889634f;
     const int page = 1 << a.g.page_log2;
 
@@ -187,7 +188,8 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts parts) {
     grid_dependency_wait();
-    const Head h = parts.head[blockIdx.x];
+    const int4 w = __ldcg(reinterpret_cast<const int4*>(parts.head) + blockIdx.x);
+    const Head h{w.x, w.y, w.z, w.w};
     if (h.b < 0) return;
     const int hk = h.item / a.row_tiles, r0 = (h.item % a.row_tiles) * a.tile_rows;
     const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -196,18 +198,18 @@ decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts part
     float m = -INFINITY;
     for (int c = first + lane; c <= h.last; c += 32) {
         const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
-        m = fmaxf(m, parts.ml[(slot * a.tile_rows + r) * 2]);
+        m = fmaxf(m, __ldcg(parts.ml + (slot * a.tile_rows + r) * 2));
     }
     m = simt::warp_max(m);
     const float ms = m == -INFINITY ? 0.f : m;
     float l = 0.f, acc[kMaxWidth / 32] = {};
     for (int c = first; c <= h.last; ++c) {
         const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
-        const float f = exp2f(parts.ml[(slot * a.tile_rows + r) * 2] - ms);
-        l = fmaf(parts.ml[(slot * a.tile_rows + r) * 2 + 1], f, l);
+        const float f = exp2f(__ldcg(parts.ml + (slot * a.tile_rows + r) * 2) - ms);
+        l = fmaf(__ldcg(parts.ml + (slot * a.tile_rows + r) * 2 + 1), f, l);
 #pragma unroll
         for (int k = 0; k < kMaxWidth / 32; ++k)
-            if (lane + 32 * k < a.dv) acc[k] = fmaf(parts.o[(slot * a.tile_rows + r) * a.dv + lane + 32 * k], f, acc[k]);
+            if (lane + 32 * k < a.dv) acc[k] = fmaf(__ldcg(parts.o + (slot * a.tile_rows + r) * a.dv + lane + 32 * k), f, acc[k]);
     }
     const size_t row = row_base(a, h.b, hk) + r0 + r;
     const float inv = l > 0.f ? 1.f / l : 0.f;

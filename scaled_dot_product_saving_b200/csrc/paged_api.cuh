@@ -60,6 +60,24 @@ size_t pool_bytes(const pg::Geometry& g, int width, attn_dtype_t dtype) {
     return (static_cast<size_t>(g.P) * g.Hkv << g.page_log2) * width * (dtype == ATTN_F32 ? 4 : 2);
 }
 
+// A programmatic dependent of the kernel before it on the stream: its launch
+// overlaps that one. Not while tracing, which would count the overlap twice.
+template <typename... P, typename... A>
+bool launch_dependent(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_trace.on ? 0 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess) return true;
+    (void)cudaGetLastError();
+    return false;
+}
+
 // ------------------------------------------------------------------ decode
 struct DecodeWorkspace {
     size_t o_off, ml_off, head_off, total;
@@ -99,24 +117,12 @@ attn_status_t decode_simt(const pg::DecodeArgs& a, const void* Q, const void* Kp
 template <typename T>
 attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg::Parts& parts, int grid,
                           cudaStream_t st) {
-    // A programmatic dependent of the decode kernel: its launch overlaps it. Not
-    // while tracing, which would count the overlap in this kernel's time.
-    cudaLaunchConfig_t cfg = {};
     constexpr int kWarps = pg::kJoinThreads / 32;
-    cfg.gridDim = dim3(grid, (std::min(a.rows, a.tile_rows) + kWarps - 1) / kWarps);
-    cfg.blockDim = dim3(pg::kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = g_trace.on ? 0 : 1;
+    const dim3 blocks(grid, (std::min(a.rows, a.tile_rows) + kWarps - 1) / kWarps);
     return traced(ATTN_KERNEL_DECODE_JOIN, st, [&] {
-        if (cudaLaunchKernelEx(&cfg, pg::decode_join<T>, a, static_cast<T*>(O), LSE, parts) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return ATTN_ERR_CUDA;
-        }
-        return launched();
+        return launch_dependent(pg::decode_join<T>, blocks, pg::kJoinThreads, st, a, static_cast<T*>(O), LSE, parts)
+                   ? launched()
+                   : ATTN_ERR_CUDA;
     });
 }
 
@@ -155,13 +161,12 @@ attn_status_t decode_tc_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, c
 
 // ------------------------------------------------------------------- books
 struct CacheWorkspace {
-    size_t first_off, after_off, start_off, base_off, key_off, stage_off, moves_off, total;
+    size_t after_off, start_off, base_off, key_off, stage_off, moves_off, total;
 };
 CacheWorkspace carve_cache(int B, int max_pages, int num_pages) {
     CacheWorkspace w;
     const auto ints = [](size_t n) { return round_up(n * sizeof(int), 256); };
-    w.first_off = ints(pg::kCtlWords);
-    w.after_off = w.first_off + ints(static_cast<size_t>(B) + 1);
+    w.after_off = ints(pg::kCtlWords);
     w.start_off = w.after_off + ints(B);
     w.base_off = w.start_off + ints(B);
     w.key_off = w.base_off + ints(num_pages);
@@ -176,8 +181,8 @@ pg::Books books(const pg::Geometry& g, const int* table, const int* lens, const 
     const CacheWorkspace w = carve_cache(g.B, g.M, g.P);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const auto at = [&](size_t off) { return reinterpret_cast<int*>(ws + off); };
-    return pg::Books{g, table, lens, ref, table_out, lens_out, ref_out, info, at(0), at(w.first_off),
-                     at(w.after_off), at(w.start_off), at(w.base_off), at(w.key_off), at(w.stage_off),
+    return pg::Books{g, table, lens, ref, table_out, lens_out, ref_out, info, at(0), at(w.after_off),
+                     at(w.start_off), at(w.base_off), at(w.key_off), at(w.stage_off),
                      reinterpret_cast<pg::Move*>(ws + w.moves_off)};
 }
 
@@ -204,13 +209,15 @@ attn_status_t launch_books(void (*kern)(P...), cudaStream_t st, A... args) {
     });
 }
 
-attn_status_t launch_moves(const pg::Books& k, void* Kp, void* Vp, int wk, int wv, long long most,
-                           cudaStream_t st) {
-    const int grid = grid_for(static_cast<size_t>(most), 1, sm_count() * 8);
+// At most `most` pages move.
+attn_status_t launch_moves(const pg::Books& k, void* Kp, void* Vp, int wk, int wv, int most, cudaStream_t st) {
+    const size_t spans = ((static_cast<size_t>(wk + wv) << k.g.page_log2) + pg::kSpan - 1) / pg::kSpan;
+    const int grid = grid_for(spans * most * k.g.Hkv, pg::kCopyThreads / 32, sm_count() * 8);
     return traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
-        pg::move_rows<<<grid, pg::kCopyThreads, 0, st>>>(k.g, static_cast<uint4*>(Kp), static_cast<uint4*>(Vp),
-                                                        k.control, k.moves, wk, wv);
-        return launched();
+        return launch_dependent(pg::move_rows, dim3(grid), pg::kCopyThreads, st, k.g, static_cast<uint4*>(Kp),
+                                static_cast<uint4*>(Vp), k.control, k.moves, wk, wv)
+                   ? launched()
+                   : ATTN_ERR_CUDA;
     });
 }
 
@@ -315,12 +322,14 @@ attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, voi
     s = launch_books(pg::append_books, st, k, new_len, n);
     if (s != ATTN_OK) return s;
     const int wk = d * es / 16, wv = dv * es / 16;
-    const int grid = grid_for(rows * (wk + wv), pg::kCopyThreads, sm_count() * 8);
+    const size_t spans = (static_cast<size_t>(n) * (wk + wv) + pg::kSpan - 1) / pg::kSpan;
+    const int grid = grid_for(spans * B * Hkv, pg::kCopyThreads / 32, sm_count() * 8);
     s = traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
-        pg::append_rows<<<grid, pg::kCopyThreads, 0, st>>>(
-            g, static_cast<const uint4*>(K), static_cast<const uint4*>(V), static_cast<uint4*>(K_pages),
-            static_cast<uint4*>(V_pages), table_out, k.control, k.start, k.after, n, wk, wv);
-        return launched();
+        return launch_dependent(pg::append_rows, dim3(grid), pg::kCopyThreads, st, g, static_cast<const uint4*>(K),
+                                static_cast<const uint4*>(V), static_cast<uint4*>(K_pages),
+                                static_cast<uint4*>(V_pages), table_out, k.control, k.start, k.after, n, wk, wv)
+                   ? launched()
+                   : ATTN_ERR_CUDA;
     });
     if (s == ATTN_OK) g_last_launches = 2;
     return s;
@@ -356,7 +365,7 @@ attn_status_t attn_cache_fork(void* K_pages, void* V_pages, const int* table, co
     s = launch_books(pg::fork_books, st, k, src, keep);
     const int es = dtype == ATTN_F32 ? 4 : 2;
     if (s == ATTN_OK)
-        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, static_cast<long long>(B) * Hkv, st);
+        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, B, st);
     if (s == ATTN_OK) g_last_launches = 2;
     return s;
 }
@@ -389,8 +398,7 @@ attn_status_t attn_cache_compact(void* K_pages, void* V_pages, const int* table,
     s = launch_books(pg::compact_books, st, k, remap);
     const int es = dtype == ATTN_F32 ? 4 : 2;
     if (s == ATTN_OK)
-        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, static_cast<long long>(num_pages) * Hkv,
-                         st);
+        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, num_pages / 2 + 1, st);
     if (s == ATTN_OK) g_last_launches = 2;
     return s;
 }

@@ -151,7 +151,7 @@ def test_in_place_and_overlaps(L):
 def test_workspace_sizes(L):
     r = lambda x: -(-x // 256) * 256
     def cache(B, M, P):
-        return (r(512) + r(4 * (B + 1)) + 2 * r(4 * B) + 2 * r(4 * P) + r(4 * B * M) + r(16 * max(B, P)))
+        return (r(512) + 2 * r(4 * B) + 2 * r(4 * P) + r(4 * B * M) + r(16 * max(B, P)))
     for args in ((1, 1, 1), (64, 1024, 20000), (300, 7, 5)):
         assert L.attn_cache_workspace_size(*args) == cache(*args)
     assert L.attn_cache_workspace_size(0, 1, 1) == 0 and L.attn_cache_workspace_size(1 << 16, 1 << 15, 1) == 0
