@@ -244,11 +244,12 @@ typedef enum {
     ATTN_KERNEL_BWD_F32X = 10,    /* ... backward: dK/dV and dQ passes, one launch */
     ATTN_KERNEL_BWD_KV = 11,      /* tcgen05 dK/dV pass (ATTN_DQ_SEPARATE)      */
     ATTN_KERNEL_BWD_DQ = 12,      /* tcgen05 dQ pass (ATTN_DQ_SEPARATE)         */
-    ATTN_KERNEL_DECODE_SIMT = 13, /* CUDA-core decode over a paged cache       */
+    ATTN_KERNEL_DECODE_SIMT = 13, /* CUDA-core decode of bf16 over a paged cache */
     ATTN_KERNEL_DECODE_JOIN = 14, /* joins the pieces of split decode items    */
     ATTN_KERNEL_CACHE_BOOKS = 15, /* table, lengths and counts of a cache call */
     ATTN_KERNEL_CACHE_ROWS = 16,  /* the rows that a cache call writes or moves */
-    ATTN_KERNEL_DECODE_TENSOR = 17 /* tensor-core decode over a paged cache    */
+    ATTN_KERNEL_DECODE_TENSOR = 17, /* tensor-core decode of bf16              */
+    ATTN_KERNEL_DECODE_F32 = 18   /* fp32 decode                               */
 } attn_kernel_id_t;
 
 typedef struct {

@@ -24,6 +24,7 @@
 #include "proj.cuh"
 #include "f32x_tc.cuh"
 #include "decode_tc.cuh"
+#include "decode_f32.cuh"
 #include "cache.cuh"
 
 namespace {

@@ -248,10 +248,14 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const i
 // The copy kernels start while the books are still being written: what they
 // read of them they read from L2, after the wait.
 //
-// A warp takes kSpan 16-byte units at a time, four a lane in flight. The units
-// of one (sequence, head), or one head of a page to move, are its rows of K and
-// then its rows of V; widths wk, wv in units.
+// A warp takes spans of kSpan 16-byte units, four a lane in flight: the rows of
+// K of one (sequence, head), or of one head of a page, and then its rows of V;
+// widths wk, wv in units.
 constexpr int kCopyThreads = 256, kSpan = 128;
+
+__host__ __device__ constexpr unsigned long long spans_of(unsigned long long units) {
+    return (units + kSpan - 1) / kSpan;
+}
 
 // New rows K [B, Hkv, n, wk], V [B, Hkv, n, wv] into their pages.
 __global__ void __launch_bounds__(kCopyThreads)
@@ -259,8 +263,8 @@ append_rows(Geometry g, const uint4* __restrict__ K, const uint4* __restrict__ V
             uint4* __restrict__ Vp, const int* table, const int* control, const int* start, const int* after,
             int n, int wk, int wv) {
     const int lane = threadIdx.x & 31, page = 1 << g.page_log2;
-    const unsigned long long units = (unsigned long long)n * (wk + wv), k_units = (unsigned long long)n * wk;
-    const unsigned long long spans = (units + kSpan - 1) / kSpan, items = spans * g.B * g.Hkv;
+    const unsigned long long k_spans = spans_of((unsigned long long)n * wk);
+    const unsigned long long spans = k_spans + spans_of((unsigned long long)n * wv), items = spans * g.B * g.Hkv;
     const unsigned long long stride = (unsigned long long)gridDim.x * (kCopyThreads / 32);
     // With one span a warp, its rows are on the way before the books are read;
     // with more, rows that turn out to be padding are not worth reading.
@@ -272,29 +276,30 @@ append_rows(Geometry g, const uint4* __restrict__ K, const uint4* __restrict__ V
     for (unsigned long long x = (unsigned long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items;
          x += stride) {
         const unsigned long long bh = x / spans;
-        const unsigned long long u0 = (x - bh * spans) * kSpan + lane;
-        const int b = int(bh / g.Hkv), h = int(bh - (unsigned long long)b * g.Hkv);
-        int t0 = 0, add = n;
+        unsigned long long span = x - bh * spans;
+        const int b = int(unsigned(bh) / unsigned(g.Hkv)), h = int(unsigned(bh) - unsigned(b) * g.Hkv);
+        const bool is_v = span >= k_spans;
+        if (is_v) span -= k_spans;
+        const unsigned w = is_v ? wv : wk;
+        // The span's first unit is column c0 of new row i0.
+        const unsigned i0 = unsigned(span * kSpan / w), c0 = unsigned(span * kSpan - (unsigned long long)i0 * w);
+        const uint4* from = (is_v ? V : K) + (bh * n + i0) * w;
+        uint4* pool = is_v ? Vp : Kp;
+        int t0 = 0;
+        unsigned add = n;
         if (!early) {
             t0 = __ldcg(start + b);
             add = __ldcg(after + b) - t0;
+            if (i0 >= add) continue;
         }
         uint4 v[4];
-        int i[4], c[4];
+        unsigned i[4], c[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const unsigned long long u = u0 + 32 * e;
-            i[e] = n;
-            if (u < k_units) {
-                i[e] = int(u / wk);
-                c[e] = int(u - (unsigned long long)i[e] * wk);
-                if (i[e] < add) v[e] = K[bh * k_units + u];
-            } else if (u < units) {
-                const unsigned long long y = u - k_units;
-                i[e] = int(y / wv);
-                c[e] = ~int(y - (unsigned long long)i[e] * wv);     // V's columns as complements
-                if (i[e] < add) v[e] = V[bh * (units - k_units) + y];
-            }
+            const unsigned u = c0 + lane + 32 * e;
+            i[e] = i0 + u / w;
+            c[e] = u % w;
+            if (i[e] < add) v[e] = from[u];
         }
         if (early) {
             grid_dependency_wait();
@@ -305,12 +310,9 @@ append_rows(Geometry g, const uint4* __restrict__ K, const uint4* __restrict__ V
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (i[e] >= add) continue;
-            const int t = t0 + i[e];
+            const int t = t0 + int(i[e]);
             const int p = __ldcg(table + size_t(b) * g.M + (t >> g.page_log2));
-            if (!page_ok(p, g.P)) continue;
-            const size_t dst = (size_t(p) * g.Hkv + h) * page + (t & (page - 1));
-            if (c[e] >= 0) Kp[dst * wk + c[e]] = v[e];
-            else Vp[dst * wv + ~c[e]] = v[e];
+            if (page_ok(p, g.P)) pool[((size_t(p) * g.Hkv + h) * page + (t & (page - 1))) * w + c[e]] = v[e];
         }
     }
 }
@@ -320,30 +322,29 @@ __global__ void __launch_bounds__(kCopyThreads)
 move_rows(Geometry g, uint4* Kp, uint4* Vp, const int* control, const Move* moves, int wk, int wv) {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const unsigned spans = ((unsigned(wk + wv) << g.page_log2) + kSpan - 1) / kSpan;
+    const unsigned k_spans = unsigned(spans_of((unsigned long long)wk << g.page_log2));
+    const unsigned spans = k_spans + unsigned(spans_of((unsigned long long)wv << g.page_log2));
     const unsigned long long items = (unsigned long long)__ldcg(control + kCtlMoves) * g.Hkv * spans;
     const unsigned long long stride = (unsigned long long)gridDim.x * (kCopyThreads / 32);
     for (unsigned long long x = (unsigned long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items;
          x += stride) {
-        const unsigned long long qh = x / spans, q = qh / g.Hkv;
-        const unsigned u0 = unsigned(x - qh * spans) * kSpan + lane;
-        const int h = int(qh - q * g.Hkv);
+        const unsigned qh = unsigned(x / spans), q = qh / unsigned(g.Hkv), h = qh - q * g.Hkv;
+        unsigned span = unsigned(x - (unsigned long long)qh * spans);
+        const bool is_v = span >= k_spans;
+        if (is_v) span -= k_spans;
+        const unsigned w = is_v ? wv : wk;
         const int4 m = __ldcg(reinterpret_cast<const int4*>(moves) + q);
-        const size_t from = (size_t(m.x) * g.Hkv + h) << g.page_log2, to = (size_t(m.y) * g.Hkv + h) << g.page_log2;
-        const unsigned k_units = unsigned(m.z) * wk, units = k_units + unsigned(m.z) * wv;
+        const unsigned units = unsigned(m.z) * w, u0 = span * kSpan + lane;
+        uint4* pool = is_v ? Vp : Kp;
+        const uint4* from = pool + ((size_t(m.x) * g.Hkv + h) << g.page_log2) * w;
+        uint4* to = pool + ((size_t(m.y) * g.Hkv + h) << g.page_log2) * w;
         uint4 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const unsigned u = u0 + 32 * e;
-            if (u < k_units) v[e] = Kp[from * wk + u];
-            else if (u < units) v[e] = Vp[from * wv + (u - k_units)];
-        }
+        for (int e = 0; e < 4; ++e)
+            if (u0 + 32 * e < units) v[e] = from[u0 + 32 * e];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const unsigned u = u0 + 32 * e;
-            if (u < k_units) Kp[to * wk + u] = v[e];
-            else if (u < units) Vp[to * wv + (u - k_units)] = v[e];
-        }
+        for (int e = 0; e < 4; ++e)
+            if (u0 + 32 * e < units) to[u0 + 32 * e] = v[e];
     }
 }
 

@@ -1,5 +1,7 @@
 // decode.cuh -- attention of the newest tokens of every sequence over its
-// paged keys and values, on the CUDA cores, and the joining of split items.
+// paged keys and values: what the kernels share, the joining of split items, and
+// the kernel for bf16 that ATTN_PATH_SIMT asks for (the others are decode_tc.cuh
+// and decode_f32.cuh).
 //
 //   S_rj = scale * q_r . k_j  over the keys j that row r may see,
 //   O_r = sum_j softmax(S_r)_j v_j,  LSE_r = ln sum_j exp(S_rj)
@@ -42,10 +44,10 @@ __host__ __device__ constexpr int simt_smem_bytes(int d, int dv) {
     return (kRows * d + kTileKeys * (d + 1) + kTileKeys * dv + kRows * kTileKeys + 3 * kRows) * 4;
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kSimtThreads)
-decode_simt(DecodeArgs a, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
-            T* __restrict__ O, float* __restrict__ LSE, Parts parts) {
+decode_simt(DecodeArgs a, const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ Kp,
+            const __nv_bfloat16* __restrict__ Vp, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE,
+            Parts parts) {
     extern __shared__ float sm[];
     __shared__ long long scratch[33], found[2];
     __shared__ int pages[kTileKeys];
@@ -153,7 +155,7 @@ decode_simt(DecodeArgs a, const T* __restrict__ Q, const T* __restrict__ Kp, con
 #pragma unroll
                 for (int r = 0; r < kRows; ++r)
                     if (r < rows && (r0 + r) % a.n < p.nq)
-                        O[(base + r) * dv + tid] = simt::from_f<T>(Ls[r] > 0.f ? acc[r] / Ls[r] : acc[r]);
+                        O[(base + r) * dv + tid] = simt::from_f<__nv_bfloat16>(Ls[r] > 0.f ? acc[r] / Ls[r] : acc[r]);
             }
             if (tid < rows && (r0 + tid) % a.n < p.nq)
                 LSE[base + tid] = (Ms[tid] + log2f(Ls[tid])) * kLn2;

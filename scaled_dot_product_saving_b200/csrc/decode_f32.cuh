@@ -1,0 +1,317 @@
+// decode_f32.cuh -- attention of the newest tokens over paged fp32 keys and
+// values, on the CUDA cores in fp32 arithmetic.
+//
+// The mathematics is decode.cuh's; the stream of tiles is decode_ring.cuh's.
+// Memory bounds it here too (1 KB a token and key head at d = 128) as long as
+// the arithmetic of a key, 2 (d + dv) fused multiply-adds per query row, keeps
+// up with 22 bytes a cycle and SM; for that neither operand of the products may
+// come from shared memory more than once:
+//  - scores: half a warp per key, 16 lanes over its width, query values of all
+//    rows in registers. The partial sums of 8 keys times 4 rows are reduced
+//    across the 16 lanes by halving: at each step a lane passes on half of its
+//    sums and adds the other half, so that 15 shuffles reduce 16 sums and leave
+//    one score per lane;
+//  - values: a lane owns 4 columns of the output for all rows, reads each value
+//    once, and the weights of a key come as one broadcast per 4 rows.
+#pragma once
+
+#include "decode_ring.cuh"
+
+namespace attn {
+namespace paged {
+
+// DK, DV: padded widths; RB: query rows of a warp (4 or 8); R: groups of RB rows.
+template <int DK, int DV, int RB, int R>
+struct DecodeF32Cfg {
+    static constexpr int kPanelCols = 32, kKPanels = DK / 32, kVPanels = DV / 32;
+    static constexpr int kKBytes = kKPanels * kPanelBytes;
+    static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
+    static constexpr int kStages = 192 * 1024 / kStageBytes;
+    static constexpr int kWarps = 8;                       // consumers: 8 / R key warps per group
+    static constexpr int kKeyWarps = kWarps / R, kWarpKeys = kTileKeys / kKeyWarps;
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kTileRows = RB * R;
+    // Half of the warps' outputs meet at a time.
+    static constexpr int kJoinBytes = kWarps / 2 * RB * DV * 4;
+    static constexpr int kOffW = kStages * kStageBytes + kJoinBytes;
+    static constexpr int kSmemBytes = kOffW + kWarps * 8 * RB * 4;
+};
+
+template <int DK, int DV, int RB, int R>
+__global__ void __launch_bounds__(DecodeF32Cfg<DK, DV, RB, R>::kThreads, 1)
+decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DecodeArgs a,
+           const float* __restrict__ Q, float* __restrict__ O, float* __restrict__ LSE, Parts parts,
+           unsigned long long budget_ns) {
+    using C = DecodeF32Cfg<DK, DV, RB, R>;
+    constexpr int kStages = C::kStages, kQ = DK / 64, kSets = RB / 4;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ long long scratch[33], found[2];
+    __shared__ Ring<kStages> ring;
+    __shared__ float stat_m[C::kWarps][RB], stat_l[C::kWarps][RB];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    Walker w;
+    if (!set_up(a, parts, ring, smem, C::kWarps, scratch, found, &w)) return;
+    if (warp == C::kWarps) {
+        produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns);
+        return;
+    }
+
+    const int kg = warp % C::kKeyWarps, group = warp / C::kKeyWarps;
+    const int s16 = lane & 15, kp = lane >> 4;             // slice of the width, key of a pair
+    const int my_row = s16 & 3, my_key = 2 * (s16 >> 2) + kp;   // of the score this lane ends with
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    float* weights = reinterpret_cast<float*>(smem + C::kOffW) + warp * 8 * RB;   // [key][row]
+    float4* joined = reinterpret_cast<float4*>(smem + kStages * C::kStageBytes);
+    constexpr int kVKeys = 128 / DV;                       // keys that a warp's 32 chunks of V cover
+    const int v_chunk = lane % (DV / 4), v_key = lane / (DV / 4);
+
+    int n = 0;
+    Piece p;
+    while (w.next(a, &p)) {
+        const int hk = p.item / a.row_tiles, r0 = (p.item % a.row_tiles) * C::kTileRows + group * RB;
+        const size_t base = row_base(a, p.b, hk);
+        const bool rows_here = r0 < a.rows;
+        // Query columns 4 (s16 + 16 x) of every row.
+        float4 q[RB][kQ];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+#pragma unroll
+            for (int x = 0; x < kQ; ++x) {
+                const int c = 4 * (s16 + 16 * x);
+                q[r][x] = r0 + r < a.rows && c < a.d
+                              ? *reinterpret_cast<const float4*>(Q + (base + r0 + r) * a.d + c)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        int see[kSets];
+        float m[kSets], l[kSets];
+        float4 acc[RB];
+#pragma unroll
+        for (int x = 0; x < kSets; ++x) {
+            see[x] = visible(a, p.len, p.nq, (r0 + 4 * x + my_row) % a.n);
+            m[x] = -INFINITY;
+            l[x] = 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < RB; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int see_all = a.causal ? p.len - (p.nq - 1) : p.len;
+
+        for (int t = p.t0; t < p.t1; ++t, ++n) {
+            const int s = n % kStages;
+            ring_wait(ring, &ring.full[s], (n / kStages) & 1, budget_ns);
+            const uint8_t* st = smem + s * C::kStageBytes;
+#pragma unroll 1
+            for (int k8 = kg * C::kWarpKeys; rows_here && k8 < (kg + 1) * C::kWarpKeys; k8 += 8) {
+                const uint32_t there = uint32_t(ring.present[s] >> k8) & 0xffu;
+                if (there == 0) continue;
+                // Scores of keys k8 + 2 pair + kp, partial over this lane's columns.
+                float part[kSets][16];
+#pragma unroll
+                for (int pair = 0; pair < 4; ++pair) {
+                    const int key = k8 + 2 * pair + kp;
+                    float4 k[kQ];
+#pragma unroll
+                    for (int x = 0; x < kQ; ++x)
+                        k[x] = *reinterpret_cast<const float4*>(st + ((s16 >> 3) + 2 * x) * kPanelBytes + key * 128 +
+                                                                (((s16 & 7) ^ (key & 7)) << 4));
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int x = 0; x < kQ; ++x) {
+                            sum = fmaf(q[r][x].x, k[x].x, sum);
+                            sum = fmaf(q[r][x].y, k[x].y, sum);
+                            sum = fmaf(q[r][x].z, k[x].z, sum);
+                            sum = fmaf(q[r][x].w, k[x].w, sum);
+                        }
+                        part[r >> 2][pair * 4 + (r & 3)] = sum;
+                    }
+                }
+                float sc[kSets];
+#pragma unroll
+                for (int x = 0; x < kSets; ++x) {
+#pragma unroll
+                    for (int o = 8; o >= 1; o >>= 1) {
+                        const bool up = s16 & o;
+#pragma unroll
+                        for (int e = 0; e < o; ++e) {
+                            const float pass = up ? part[x][e] : part[x][e + o];
+                            const float stay = up ? part[x][e + o] : part[x][e];
+                            part[x][e] = stay + __shfl_xor_sync(0xffffffffu, pass, o);
+                        }
+                    }
+                    sc[x] = part[x][0] * scale_log2;       // row 4 x + my_row, key k8 + my_key
+                }
+                const int k0 = t * kTileKeys + k8;
+                const bool whole = there == 0xffu && k0 + 8 <= see_all;
+                if (!whole) {
+#pragma unroll
+                    for (int x = 0; x < kSets; ++x)
+                        if (!(there >> my_key & 1) || k0 + my_key >= see[x]) sc[x] = -INFINITY;
+                }
+                // Running maximum over the keys of a row (lanes that differ in bits
+                // 2, 3 and 4); the reference moves when it has grown by more than 8.
+                float top[kSets];
+                bool grown = false;
+#pragma unroll
+                for (int x = 0; x < kSets; ++x) {
+                    top[x] = sc[x];
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], o));
+                    grown |= top[x] > m[x] + 8.f;
+                }
+                if (__any_sync(0xffffffffu, grown)) {
+                    float f[kSets];
+#pragma unroll
+                    for (int x = 0; x < kSets; ++x) {
+                        const float next = fmaxf(m[x], top[x]);
+                        f[x] = next == -INFINITY ? 1.f : exp2f(m[x] - next);
+                        m[x] = next;
+                        l[x] *= f[x];
+                    }
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) {
+                        const float fr = __shfl_sync(0xffffffffu, f[r >> 2], r & 3);
+                        acc[r].x *= fr;
+                        acc[r].y *= fr;
+                        acc[r].z *= fr;
+                        acc[r].w *= fr;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kSets; ++x) {
+                    const float e = exp2f(sc[x] - (m[x] == -INFINITY ? 0.f : m[x]));
+                    l[x] += e;
+                    weights[my_key * RB + 4 * x + my_row] = e;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j0 = 0; j0 < 8; j0 += kVKeys) {
+                    const int j = j0 + v_key, key = k8 + j;
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        st + C::kKBytes + (v_chunk >> 3) * kPanelBytes + key * 128 + (((v_chunk & 7) ^ (key & 7)) << 4));
+                    if (!whole && !(there >> j & 1)) continue;     // a row that no token owns may hold anything
+#pragma unroll
+                    for (int x = 0; x < kSets; ++x) {
+                        const float4 e4 = *reinterpret_cast<const float4*>(weights + j * RB + 4 * x);
+                        const float e[4] = {e4.x, e4.y, e4.z, e4.w};
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            // ... and a token that only some rows see
+                            if (!whole && e[r] == 0.f) continue;
+                            float4& o = acc[4 * x + r];
+                            o.x = fmaf(e[r], v.x, o.x);
+                            o.y = fmaf(e[r], v.y, o.y);
+                            o.z = fmaf(e[r], v.z, o.z);
+                            o.w = fmaf(e[r], v.w, o.w);
+                        }
+                    }
+                }
+                __syncwarp();                              // weights are read before the next 8 keys'
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ring.empty[s]);
+        }
+
+        // ------------------------------------------ the group's warps joined
+#pragma unroll
+        for (int x = 0; x < kSets; ++x) {
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
+            if (lane < 4) {
+                stat_m[warp][4 * x + lane] = m[x];
+                stat_l[warp][4 * x + lane] = l[x];
+            }
+        }
+        if constexpr (kVKeys == 2) {                       // the two keys' halves of the output
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                acc[r].x += __shfl_xor_sync(0xffffffffu, acc[r].x, 16);
+                acc[r].y += __shfl_xor_sync(0xffffffffu, acc[r].y, 16);
+                acc[r].z += __shfl_xor_sync(0xffffffffu, acc[r].z, 16);
+                acc[r].w += __shfl_xor_sync(0xffffffffu, acc[r].w, 16);
+            }
+        }
+        constexpr int kGroup = C::kKeyWarps;               // warps that are joined, ids 1 + group
+        const int w0 = group * kGroup, bar = R == 1 ? 1 : 1 + group;
+        auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(kGroup * 32) : "memory"); };
+        meet();
+        float M[RB], L[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            M[r] = -INFINITY;
+            L[r] = 0.f;
+            for (int x = 0; x < kGroup; ++x) M[r] = fmaxf(M[r], stat_m[w0 + x][r]);
+            const float z = M[r] == -INFINITY ? 0.f : M[r];
+            for (int x = 0; x < kGroup; ++x) L[r] = fmaf(stat_l[w0 + x][r], exp2f(stat_m[w0 + x][r] - z), L[r]);
+            const float f = exp2f(stat_m[warp][r] - z);
+            acc[r].x *= f;
+            acc[r].y *= f;
+            acc[r].z *= f;
+            acc[r].w *= f;
+        }
+        // The upper half of the warps leaves its outputs, the lower half adds its
+        // own and leaves the sums, and every warp takes some rows of their sum.
+        constexpr int kHalf = kGroup / 2, kChunks = DV / 4;
+        float4* mine = joined + (group * kHalf + kg % kHalf) * (RB * kChunks);
+        if (kg >= kHalf && lane < kChunks) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) mine[r * kChunks + lane] = acc[r];
+        }
+        meet();
+        if (kg < kHalf && lane < kChunks) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const float4 o = mine[r * kChunks + lane];
+                mine[r * kChunks + lane] = make_float4(acc[r].x + o.x, acc[r].y + o.y, acc[r].z + o.z, acc[r].w + o.w);
+            }
+        }
+        meet();
+        const bool all = p.t0 == 0 && p.t1 == p.tiles;
+        const size_t slot = 2 * size_t(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int row = r0 + r;
+            if (r % kGroup != kg || row >= a.rows) continue;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < kChunks) {
+#pragma unroll
+                for (int x = 0; x < kHalf; ++x) {
+                    const float4 y = joined[((group * kHalf + x) * RB + r) * kChunks + lane];
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                }
+            }
+            if (all) {
+                if (row % a.n >= p.nq) continue;
+                const float inv = L[r] > 0.f ? 1.f / L[r] : L[r] == 0.f ? 0.f : L[r];    // NaN stays
+                if (4 * lane < a.dv)
+                    *reinterpret_cast<float4*>(O + (base + row) * a.dv + 4 * lane) =
+                        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                if (lane == 0) LSE[base + row] = (M[r] + log2f(L[r])) * kLn2;
+            } else {
+                const size_t at = slot * C::kTileRows + group * RB + r;
+                if (4 * lane < a.dv) *reinterpret_cast<float4*>(parts.o + at * a.dv + 4 * lane) = o;
+                if (lane == 0) {
+                    parts.ml[at * 2] = M[r];
+                    parts.ml[at * 2 + 1] = L[r];
+                }
+            }
+        }
+        if (!all && p.t0 == 0 && warp == 0 && lane == 0) {
+            Head h;
+            h.b = p.b;
+            h.item = p.item;
+            h.nq = p.nq;
+            h.last = w.owner(p.end - 1);
+            parts.head[blockIdx.x] = h;
+        }
+        meet();                                            // sums and statistics are read
+    }
+}
+
+}  // namespace paged
+}  // namespace attn

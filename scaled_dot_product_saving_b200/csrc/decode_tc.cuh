@@ -23,7 +23,7 @@
 // from HBM (a 32 KB tile every 1,450 cycles).
 #pragma once
 
-#include "decode.cuh"
+#include "decode_ring.cuh"
 
 namespace attn {
 namespace paged {
@@ -32,9 +32,9 @@ constexpr int kKeyWarps = 4;                       // warps that share a tile's 
 
 template <int DK, int DV, int R>                   // padded widths, groups of 16 query rows
 struct DecodeCfg {
-    static constexpr int kPanelBytes = kTileKeys * 128;
-    static constexpr int kKBytes = DK / 64 * kPanelBytes;
-    static constexpr int kStageBytes = kKBytes + DV / 64 * kPanelBytes;
+    static constexpr int kPanelCols = 64, kKPanels = DK / 64, kVPanels = DV / 64;
+    static constexpr int kKBytes = kKPanels * kPanelBytes;
+    static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
     static constexpr int kThreads = (kKeyWarps * R + 1) * 32;
     // Two CTAs an SM for 16 rows (96 KB of stages each), one for more.
     static constexpr int kCtasPerSm = R == 1 ? 2 : 1;
@@ -84,102 +84,15 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     constexpr int kTileRows = 16 * R, kStages = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ long long scratch[33], found[2];
-    __shared__ uint64_t full[kStages], empty[kStages];
-    __shared__ unsigned long long present[kStages];       // keys of the stage that exist
+    __shared__ Ring<kStages> ring;
     __shared__ float stat_m[R][kKeyWarps][16], stat_l[R][kKeyWarps][16];
-    __shared__ int abort_flag_s;
-    volatile int* abort_flag = &abort_flag_s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (tid == 0) {
-        parts.head[blockIdx.x].b = -1;
-        const bool misaligned = (smem_addr(smem) & 1023u) != 0;
-        if (misaligned) record_device_error(kErrTimeout);
-        abort_flag_s = misaligned || *reinterpret_cast<volatile unsigned int*>(&g_device_error) != 0;
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kKeyWarps * R);
-        }
-        fence_mbar_init();
-    }
     Walker w;
-    w.start(a, scratch, found);                           // ends with a barrier
-    if (abort_flag_s) return;
-    __syncthreads();                                      // every thread has read the flag
-    grid_launch_dependents();                             // the join may set up meanwhile
+    if (!set_up(a, parts, ring, smem, kKeyWarps * R, scratch, found, &w)) return;
 
-    // A wait that runs out sets the flag, after which every wait returns at
-    // once: each role goes through its loops without data, so that no thread
-    // stays behind at a barrier, and the error word tells the host.
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!mbar_wait(bar, parity, abort_flag, budget_ns)) {
-            record_device_error(kErrTimeout);
-            *abort_flag = 1;
-        }
-    };
-
-    const int page_log2 = a.g.page_log2, page = 1 << page_log2;
     if (warp == kKeyWarps * R) {
-        // ------------------------------------------------------ TMA producer
-        // A tile is 64 / box pages (box = min(page, 64) tokens, one lane each).
-        // 32 table entries are held across the warp and the next 32 on the way.
-        const int box = min(page, kTileKeys), boxes = kTileKeys / box;
-        const int box_log2 = min(page_log2, 6);
-        if (lane == 0) {
-            prefetch_tensor_map(&tmK);
-            prefetch_tensor_map(&tmV);
-        }
-        int n = 0;                                        // tiles issued
-        Piece p;
-        while (w.next(a, &p)) {
-            const int hk = p.item / a.row_tiles;
-            const int* row = a.table + size_t(p.b) * a.g.M;
-            const int last = pages_of(p.len, page_log2);
-            int base = (p.t0 * kTileKeys) >> page_log2;
-            int held = base + lane < last ? row[base + lane] : -1;
-            int ahead = base + 32 + lane < last ? row[base + 32 + lane] : -1;
-            for (int t = p.t0; t < p.t1; ++t, ++n) {
-                const int k0 = t * kTileKeys, first = k0 >> page_log2;
-                if (first - base >= 32) {
-                    base += 32;
-                    held = ahead;
-                    ahead = base + 32 + lane < last ? row[base + 32 + lane] : -1;
-                }
-                const int key = k0 + (lane << box_log2);
-                const int entry = __shfl_sync(0xffffffffu, held, (key >> page_log2) - base);
-                const bool load = lane < boxes && key < p.len && page_ok(entry, a.g.P);
-                const unsigned loads = __ballot_sync(0xffffffffu, load);
-                const int s = n % kStages;
-                if (n >= kStages) wait(&empty[s], (n / kStages - 1) & 1);
-                const bool go = __all_sync(0xffffffffu, !*abort_flag);
-                if (lane == 0) {
-                    unsigned long long keys = ~0ull;
-                    if (loads != (1u << boxes) - 1u) {
-                        const unsigned long long one = box == 64 ? ~0ull : (1ull << box) - 1ull;
-                        keys = 0;
-                        for (int x = 0; x < boxes; ++x)
-                            if (loads >> x & 1) keys |= one << (x << box_log2);
-                    }
-                    if (p.len - k0 < kTileKeys) keys &= p.len > k0 ? (1ull << (p.len - k0)) - 1ull : 0ull;
-                    present[s] = keys;
-                    mbar_arrive_expect_tx(&full[s], go ? __popc(loads) * box * (DK + DV) * 2 : 0);
-                }
-                __syncwarp();
-                if (load && go) {
-                    uint8_t* dst = smem + s * C::kStageBytes + (lane << box_log2) * 128;
-                    const int z = entry * a.g.Hkv + hk, y = key & (page - 1);
-#pragma unroll
-                    for (int x = 0; x < DK / 64; ++x)
-                        tma_load_3d(dst + x * C::kPanelBytes, &tmK, &full[s], 64 * x, y, z);
-#pragma unroll
-                    for (int x = 0; x < DV / 64; ++x)
-                        tma_load_3d(dst + C::kKBytes + x * C::kPanelBytes, &tmV, &full[s], 64 * x, y, z);
-                }
-            }
-        }
-        // No copy may be in flight into shared memory that the CTA gives back.
-        for (int x = max(0, n - kStages); x < n; ++x)
-            (void)mbar_wait_timed(&full[x % kStages], (x / kStages) & 1, budget_ns);
+        produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns);
         return;
     }
 
@@ -237,16 +150,16 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
 
         for (int t = p.t0; t < p.t1; ++t, ++n) {
             const int s = n % kStages;
-            wait(&full[s], (n / kStages) & 1);
+            ring_wait(ring, &ring.full[s], (n / kStages) & 1, budget_ns);
             const uint32_t st = sm + s * C::kStageBytes;
             const int k0 = t * kTileKeys + kg * 16;       // this warp's keys
-            const uint32_t there = uint32_t(present[s] >> (kg * 16)) & 0xffffu;
+            const uint32_t there = uint32_t(ring.present[s] >> (kg * 16)) & 0xffffu;
             if (rows_here && there != 0) {
                 float sc[2][4] = {};
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     uint32_t b[4];
-                    ldsm4(st + (ks / 4) * C::kPanelBytes + k_row + (k_x ^ ((ks & 3) << 5)), b);
+                    ldsm4(st + (ks / 4) * kPanelBytes + k_row + (k_x ^ ((ks & 3) << 5)), b);
                     uint32_t(&q)[4] = qf[C::kQShared ? 0 : ks];
                     if constexpr (C::kQShared) ldsm4(q_at + ks * 32, q);
                     mma16816(sc[0], q, b[0], b[1]);
@@ -310,7 +223,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
 #pragma unroll
                     for (int c = 0; c < DV / 16; ++c) {
                         uint32_t b[4];
-                        ldsm4_t(st + (c / 4) * C::kPanelBytes + v_row + (v_x ^ ((c & 3) << 5)), b);
+                        ldsm4_t(st + (c / 4) * kPanelBytes + v_row + (v_x ^ ((c & 3) << 5)), b);
                         mma16816(acc[2 * c], pf, b[0], b[1]);
                         mma16816(acc[2 * c + 1], pf, b[2], b[3]);
                     }
@@ -326,7 +239,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
 #pragma unroll
                     for (int c = 0; c < DV / 16; ++c) {
                         uint32_t b[4];
-                        ldsm4_t(st + (c / 4) * C::kPanelBytes + v_row + (v_x ^ ((c & 3) << 5)), b);
+                        ldsm4_t(st + (c / 4) * kPanelBytes + v_row + (v_x ^ ((c & 3) << 5)), b);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             b[x] &= x & 1 ? hi : lo;
@@ -352,7 +265,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                             const int key = kg * 16 + j;
 #pragma unroll
                             for (int c = 0; c < DV / 8; ++c) {
-                                const uint8_t* at = smem + s * C::kStageBytes + C::kKBytes + (c / 8) * C::kPanelBytes +
+                                const uint8_t* at = smem + s * C::kStageBytes + C::kKBytes + (c / 8) * kPanelBytes +
                                                     key * 128 + (((c & 7) ^ (key & 7)) << 4) + t4 * 4;
                                 const uint32_t v = *reinterpret_cast<const uint32_t*>(at);
 #pragma unroll
@@ -368,7 +281,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
+            if (lane == 0) mbar_arrive(&ring.empty[s]);
         }
 
         // ------------------------------------------- the four warps joined

@@ -100,16 +100,17 @@ attn_status_t check_decode(int B, int H, int Hkv, int n, int d, int dv, attn_dty
     return ATTN_OK;
 }
 
-template <typename T>
 attn_status_t decode_simt(const pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O,
-                          float* LSE, const pg::Parts& parts, int grid, cudaStream_t st) {
+                          float* LSE, const pg::Parts& parts, int* grid, cudaStream_t st) {
     const int smem = pg::simt_smem_bytes(a.d, a.dv);
-    auto kern = pg::decode_simt<T>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(pg::decode_simt, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return ATTN_ERR_CUDA;
+    *grid = std::min(2 * sm_count(), kDecodeCtas);
     return traced(ATTN_KERNEL_DECODE_SIMT, st, [&] {
-        kern<<<grid, pg::kSimtThreads, smem, st>>>(a, static_cast<const T*>(Q), static_cast<const T*>(Kp),
-                                                   static_cast<const T*>(Vp), static_cast<T*>(O), LSE, parts);
+        using T = __nv_bfloat16;
+        pg::decode_simt<<<*grid, pg::kSimtThreads, smem, st>>>(a, static_cast<const T*>(Q), static_cast<const T*>(Kp),
+                                                               static_cast<const T*>(Vp), static_cast<T*>(O), LSE,
+                                                               parts);
         return launched();
     });
 }
@@ -126,36 +127,60 @@ attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg
     });
 }
 
-template <int DK, int DV, int R>
-attn_status_t decode_tc(const pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
-                        const pg::Parts& parts, int* grid, cudaStream_t st) {
-    using C = pg::DecodeCfg<DK, DV, R>;
+// The kernels that stream tiles with the TMA. C: the kernel's configuration; T:
+// the element type, whose columns the maps' 128-byte rows hold.
+template <typename C, typename T, typename Kern>
+attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg::DecodeArgs& a, const void* Q,
+                            const void* Kp, const void* Vp, void* O, float* LSE, const pg::Parts& parts, int* grid,
+                            cudaStream_t st) {
     CUtensorMap mk, mv;
     const int page = 1 << a.g.page_log2, heads = a.g.P * a.g.Hkv, box = std::min(page, pg::kTileKeys);
-    if (!make_map_typed(&mk, Kp, a.d, page, heads, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, box) ||
-        !make_map_typed(&mv, Vp, a.dv, page, heads, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, box))
+    constexpr auto type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_map_typed(&mk, Kp, a.d, page, heads, type, sizeof(T), C::kPanelCols, box) ||
+        !make_map_typed(&mv, Vp, a.dv, page, heads, type, sizeof(T), C::kPanelCols, box))
         return ATTN_ERR_CUDA;
-    auto kern = pg::decode_tc<DK, DV, R>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    *grid = std::min(C::kCtasPerSm * sm_count(), std::min(kDecodeCtas, kDecodeRows / (16 * R)));
-    return traced(ATTN_KERNEL_DECODE_TENSOR, st, [&] {
-        kern<<<*grid, C::kThreads, C::kSmemBytes, st>>>(mk, mv, a, static_cast<const __nv_bfloat16*>(Q),
-                                                        static_cast<__nv_bfloat16*>(O), LSE, parts, kWaitBudgetNs);
+    *grid = std::min(ctas_per_sm * sm_count(), std::min(kDecodeCtas, kDecodeRows / a.tile_rows));
+    return traced(kernel_id, st, [&] {
+        kern<<<*grid, C::kThreads, C::kSmemBytes, st>>>(mk, mv, a, static_cast<const T*>(Q), static_cast<T*>(O), LSE,
+                                                        parts, kWaitBudgetNs);
         return launched();
     });
 }
 
-// Query rows of an item: as many of a key head's as there are, up to 64, since
-// every item reads its keys again.
-template <int DK, int DV>
-attn_status_t decode_tc_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
-                             const pg::Parts& parts, int* grid, cudaStream_t st) {
-    const int r = a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4;
-    a.tile_rows = 16 * r;
+template <int DK, int DV, int R>
+attn_status_t decode_tc(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
+                        const pg::Parts& parts, int* grid, cudaStream_t st) {
+    using C = pg::DecodeCfg<DK, DV, R>;
+    a.tile_rows = 16 * R;
     a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
-    if (r == 1) return decode_tc<DK, DV, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
-    if (r == 2) return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    return decode_stream<C, __nv_bfloat16>(pg::decode_tc<DK, DV, R>, ATTN_KERNEL_DECODE_TENSOR, C::kCtasPerSm, a, Q,
+                                           Kp, Vp, O, LSE, parts, grid, st);
+}
+
+template <int DK, int DV, int RB, int R>
+attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
+                         const pg::Parts& parts, int* grid, cudaStream_t st) {
+    using C = pg::DecodeF32Cfg<DK, DV, RB, R>;
+    a.tile_rows = RB * R;
+    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
+    return decode_stream<C, float>(pg::decode_f32<DK, DV, RB, R>, ATTN_KERNEL_DECODE_F32, 1, a, Q, Kp, Vp, O, LSE,
+                                   parts, grid, st);
+}
+
+// Query rows of an item: as many of a key head's as there are, up to 64 (bf16)
+// or 16 (fp32), since every item reads its keys again.
+template <int DK, int DV>
+attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
+                          const pg::Parts& parts, int* grid, bool f32, cudaStream_t st) {
+    if (f32) {
+        if (a.rows <= 4) return decode_f32<DK, DV, 4, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+        if (a.rows <= 8) return decode_f32<DK, DV, 8, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+        return decode_f32<DK, DV, 8, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    }
+    if (a.rows <= 16) return decode_tc<DK, DV, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    if (a.rows <= 32) return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
     return decode_tc<DK, DV, 4>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
 }
 
@@ -211,7 +236,8 @@ attn_status_t launch_books(void (*kern)(P...), cudaStream_t st, A... args) {
 
 // At most `most` pages move.
 attn_status_t launch_moves(const pg::Books& k, void* Kp, void* Vp, int wk, int wv, int most, cudaStream_t st) {
-    const size_t spans = ((static_cast<size_t>(wk + wv) << k.g.page_log2) + pg::kSpan - 1) / pg::kSpan;
+    const size_t spans = pg::spans_of(static_cast<size_t>(wk) << k.g.page_log2) +
+                         pg::spans_of(static_cast<size_t>(wv) << k.g.page_log2);
     const int grid = grid_for(spans * most * k.g.Hkv, pg::kCopyThreads / 32, sm_count() * 8);
     return traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
         return launch_dependent(pg::move_rows, dim3(grid), pg::kCopyThreads, st, k.g, static_cast<uint4*>(Kp),
@@ -249,12 +275,12 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
 
     // bf16 runs on the tensor cores, fp32 on the CUDA cores; attn_set_path holds here too.
-    const bool tensor = dtype == ATTN_BF16 && g_path != ATTN_PATH_SIMT;
-    if (g_path == ATTN_PATH_TENSOR && !tensor) return ATTN_ERR_UNSUPPORTED;
+    const bool f32 = dtype == ATTN_F32;
+    if (g_path == ATTN_PATH_TENSOR && f32) return ATTN_ERR_UNSUPPORTED;
     pg::DecodeArgs a{g, table, lens, q_len, H, n, d, dv, H / Hkv * n, pg::kRows, 0, causal != 0, scale};
-    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
+    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;      // the kernels' tiles may differ by a factor of 4
     // The kernel numbers its units (key tiles of all items) times CTAs in 64 bits.
-    if (static_cast<double>(B) * Hkv * a.row_tiles * ((static_cast<double>(max_pages) * page) / pg::kTileKeys + 1) >=
+    if (4.0 * B * Hkv * a.row_tiles * ((static_cast<double>(max_pages) * page) / pg::kTileKeys + 1) >=
         9007199254740992.0)
         return ATTN_ERR_SHAPE;
     const size_t es = dtype == ATTN_F32 ? 4 : 2, rows = static_cast<size_t>(B) * H * n;
@@ -268,19 +294,17 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const pg::Parts parts{reinterpret_cast<float*>(ws + w.o_off), reinterpret_cast<float*>(ws + w.ml_off),
                           reinterpret_cast<pg::Head*>(ws + w.head_off)};
-    int grid = std::min(2 * sm_count(), kDecodeCtas);
-    if (tensor)
-        s = d <= 64 ? (dv <= 64 ? decode_tc_rows<64, 64>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st)
-                                : decode_tc_rows<64, 128>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st))
-                    : (dv <= 64 ? decode_tc_rows<128, 64>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st)
-                                : decode_tc_rows<128, 128>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st));
-    else if (dtype == ATTN_F32)
-        s = decode_simt<float>(a, Q, K_pages, V_pages, O, LSE, parts, grid, st);
+    int grid = 0;
+    if (!f32 && g_path == ATTN_PATH_SIMT)
+        s = decode_simt(a, Q, K_pages, V_pages, O, LSE, parts, &grid, st);
+    else if (d <= 64)
+        s = dv <= 64 ? decode_rows<64, 64>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, f32, st)
+                     : decode_rows<64, 128>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, f32, st);
     else
-        s = decode_simt<__nv_bfloat16>(a, Q, K_pages, V_pages, O, LSE, parts, grid, st);
+        s = dv <= 64 ? decode_rows<128, 64>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, f32, st)
+                     : decode_rows<128, 128>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, f32, st);
     if (s == ATTN_OK)
-        s = dtype == ATTN_F32 ? decode_join<float>(a, O, LSE, parts, grid, st)
-                              : decode_join<__nv_bfloat16>(a, O, LSE, parts, grid, st);
+        s = f32 ? decode_join<float>(a, O, LSE, parts, grid, st) : decode_join<__nv_bfloat16>(a, O, LSE, parts, grid, st);
     if (s == ATTN_OK) g_last_launches = 2;
     return s;
 }
@@ -322,7 +346,7 @@ attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, voi
     s = launch_books(pg::append_books, st, k, new_len, n);
     if (s != ATTN_OK) return s;
     const int wk = d * es / 16, wv = dv * es / 16;
-    const size_t spans = (static_cast<size_t>(n) * (wk + wv) + pg::kSpan - 1) / pg::kSpan;
+    const size_t spans = pg::spans_of(static_cast<size_t>(n) * wk) + pg::spans_of(static_cast<size_t>(n) * wv);
     const int grid = grid_for(spans * B * Hkv, pg::kCopyThreads / 32, sm_count() * 8);
     s = traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
         return launch_dependent(pg::append_rows, dim3(grid), pg::kCopyThreads, st, g, static_cast<const uint4*>(K),
