@@ -49,7 +49,6 @@ decode_simt(DecodeArgs a, const __nv_bfloat16* __restrict__ Q, const __nv_bfloat
             const __nv_bfloat16* __restrict__ Vp, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE,
             Parts parts) {
     extern __shared__ float sm[];
-    __shared__ long long scratch[33], found[2];
     __shared__ int pages[kTileKeys];
     const int d = a.d, dv = a.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float* Qs = sm;                              // [16][d]
@@ -60,8 +59,9 @@ decode_simt(DecodeArgs a, const __nv_bfloat16* __restrict__ Q, const __nv_bfloat
     float* Ls = Ms + kRows;                      // [16] sum
     float* Cs = Ls + kRows;                      // [16] factor of the old sums
 
+    // Every warp walks the CTA's pieces.
     Walker w;
-    w.start(a, scratch, found);
+    w.start(a);
     if (tid == 0) parts.head[blockIdx.x].b = -1;
     grid_launch_dependents();
     const float scale_log2 = a.scale * 1.4426950408889634f;
@@ -181,43 +181,90 @@ decode_simt(DecodeArgs a, const __nv_bfloat16* __restrict__ Q, const __nv_bfloat
     }
 }
 
-// One warp per row of the item that starts in CTA blockIdx.x and goes on:
-// O = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over its pieces, in the
-// order of the CTAs, so that a repeated call gives the same bits.
+// The item that starts in CTA blockIdx.x and goes on, a row on `split` warps:
+// O = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over its pieces, in an order
+// that only depends on their number, so that a repeated call gives the same
+// bits. What bounds it is latency: up to 32 maxima and sums are read at once,
+// and eight pieces' rows.
 constexpr int kJoinThreads = 128;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
-decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts parts) {
+decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts parts, int split) {
+    __shared__ float4 sums[kJoinThreads];
     grid_dependency_wait();
-    const int4 w = __ldcg(reinterpret_cast<const int4*>(parts.head) + blockIdx.x);
-    const Head h{w.x, w.y, w.z, w.w};
-    if (h.b < 0) return;
+    const int4 hw = __ldcg(reinterpret_cast<const int4*>(parts.head) + blockIdx.x);
+    const Head h{hw.x, hw.y, hw.z, hw.w};
+    if (h.b < 0) return;                                    // the whole block
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = h.item / a.row_tiles, r0 = (h.item % a.row_tiles) * a.tile_rows;
-    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= min(a.tile_rows, a.rows - r0) || (r0 + r) % a.n >= h.nq) return;
-    const int first = blockIdx.x;
-    float m = -INFINITY;
-    for (int c = first + lane; c <= h.last; c += 32) {
-        const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
-        m = fmaxf(m, __ldcg(parts.ml + (slot * a.tile_rows + r) * 2));
-    }
-    m = simt::warp_max(m);
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[kMaxWidth / 32] = {};
-    for (int c = first; c <= h.last; ++c) {
-        const size_t slot = c == first ? 2 * size_t(c) + 1 : 2 * size_t(c);
-        const float f = exp2f(__ldcg(parts.ml + (slot * a.tile_rows + r) * 2) - ms);
-        l = fmaf(__ldcg(parts.ml + (slot * a.tile_rows + r) * 2 + 1), f, l);
+    const int r = (blockIdx.y * (kJoinThreads / 32) + warp) / split, part = warp % split;
+    const bool live = r < min(a.tile_rows, a.rows - r0) && (r0 + r) % a.n < h.nq;
+    const int first = blockIdx.x, pieces = h.last - first + 1;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+        auto row_of = [&](int c) {
+            return (2 * size_t(first + c) + (c == 0 ? 1 : 0)) * a.tile_rows + r;
+        };
+        const float2* ml = reinterpret_cast<const float2*>(parts.ml);
+        for (int c = lane; c < pieces; c += 32) m = fmaxf(m, __ldcg(&ml[row_of(c)].x));
+        m = simt::warp_max(m);
+        const float ms = m == -INFINITY ? 0.f : m;
+        for (int c0 = 0; c0 < pieces; c0 += 32) {
+            float w = 0.f;
+            if (c0 + lane < pieces) {
+                const float2 x = __ldcg(ml + row_of(c0 + lane));
+                w = exp2f(x.x - ms);
+                l = fmaf(x.y, w, l);
+            }
+            const int end = min(32, pieces - c0);
+            for (int c = part; c < end; c += 8 * split) {
+                float4 o[8];
 #pragma unroll
-        for (int k = 0; k < kMaxWidth / 32; ++k)
-            if (lane + 32 * k < a.dv) acc[k] = fmaf(__ldcg(parts.o + (slot * a.tile_rows + r) * a.dv + lane + 32 * k), f, acc[k]);
+                for (int e = 0; e < 8; ++e) {
+                    o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c + e * split < end && 4 * lane < a.dv)
+                        o[e] = __ldcg(reinterpret_cast<const float4*>(
+                            parts.o + row_of(c0 + c + e * split) * a.dv + 4 * lane));
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float f = __shfl_sync(0xffffffffu, w, (c + e * split) & 31);
+                    if (c + e * split >= end) continue;
+                    acc.x = fmaf(o[e].x, f, acc.x);
+                    acc.y = fmaf(o[e].y, f, acc.y);
+                    acc.z = fmaf(o[e].z, f, acc.z);
+                    acc.w = fmaf(o[e].w, f, acc.w);
+                }
+            }
+        }
+        l = simt::warp_sum(l);
     }
+    if (split > 1) {
+        sums[threadIdx.x] = acc;
+        __syncthreads();
+        if (part != 0) return;
+        for (int x = 1; x < split; ++x) {
+            const float4 o = sums[threadIdx.x + 32 * x];
+            acc.x += o.x;
+            acc.y += o.y;
+            acc.z += o.z;
+            acc.w += o.w;
+        }
+    }
+    if (!live) return;
     const size_t row = row_base(a, h.b, hk) + r0 + r;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int k = 0; k < kMaxWidth / 32; ++k)
-        if (lane + 32 * k < a.dv) O[row * a.dv + lane + 32 * k] = simt::from_f<T>(acc[k] * inv);
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;           // NaN stays
+    if (4 * lane < a.dv) {
+        T* o = O + row * a.dv + 4 * lane;
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(o) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        } else {
+            *reinterpret_cast<uint2*>(o) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+    }
     if (lane == 0) LSE[row] = (m + log2f(l)) * kLn2;
 }
 

@@ -31,9 +31,9 @@ struct DecodeF32Cfg {
     static constexpr int kKeyWarps = kWarps / R, kWarpKeys = kTileKeys / kKeyWarps;
     static constexpr int kThreads = (kWarps + 1) * 32;
     static constexpr int kTileRows = RB * R;
-    // Half of the warps' outputs meet at a time.
-    static constexpr int kJoinBytes = kWarps / 2 * RB * DV * 4;
-    static constexpr int kOffW = kStages * kStageBytes + kJoinBytes;
+    // The warps' outputs, when a piece ends, lie in the stage of its last tile.
+    static_assert(kWarps * RB * DV * 4 <= kStageBytes, "outputs larger than a stage");
+    static constexpr int kOffW = kStages * kStageBytes;
     static constexpr int kSmemBytes = kOffW + kWarps * 8 * RB * 4;
 };
 
@@ -45,15 +45,15 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     using C = DecodeF32Cfg<DK, DV, RB, R>;
     constexpr int kStages = C::kStages, kQ = DK / 64, kSets = RB / 4;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long scratch[33], found[2];
-    __shared__ Ring<kStages> ring;
+    __shared__ Ring<kStages, 1> ring;                      // all groups meet, since they share the stage
     __shared__ float stat_m[C::kWarps][RB], stat_l[C::kWarps][RB];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     Walker w;
-    if (!set_up(a, parts, ring, smem, C::kWarps, scratch, found, &w)) return;
+    if (warp == C::kWarps) w.start(a);                     // while the barriers are set up
+    if (!set_up(parts, ring, smem, C::kWarps)) return;
     if (warp == C::kWarps) {
-        produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns);
+        produce<C>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns);
         return;
     }
 
@@ -62,48 +62,135 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     const int my_row = s16 & 3, my_key = 2 * (s16 >> 2) + kp;   // of the score this lane ends with
     const float scale_log2 = a.scale * 1.4426950408889634f;
     float* weights = reinterpret_cast<float*>(smem + C::kOffW) + warp * 8 * RB;   // [key][row]
-    float4* joined = reinterpret_cast<float4*>(smem + kStages * C::kStageBytes);
     constexpr int kVKeys = 128 / DV;                       // keys that a warp's 32 chunks of V cover
     const int v_chunk = lane % (DV / 4), v_key = lane / (DV / 4);
 
-    int n = 0;
-    Piece p;
-    while (w.next(a, &p)) {
-        const int hk = p.item / a.row_tiles, r0 = (p.item % a.row_tiles) * C::kTileRows + group * RB;
-        const size_t base = row_base(a, p.b, hk);
-        const bool rows_here = r0 < a.rows;
-        // Query columns 4 (s16 + 16 x) of every row.
-        float4 q[RB][kQ];
+    At at{};
+    uint32_t joints = 0;                                   // parity of the next meeting
+    int tile0 = 0, see_all = 0;
+    float4 q[RB][kQ];
+    int see[kSets];
+    float m[kSets], l[kSets];
+    float4 acc[RB];
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-#pragma unroll
-            for (int x = 0; x < kQ; ++x) {
-                const int c = 4 * (s16 + 16 * x);
-                q[r][x] = r0 + r < a.rows && c < a.d
-                              ? *reinterpret_cast<const float4*>(Q + (base + r0 + r) * a.d + c)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        }
-        int see[kSets];
-        float m[kSets], l[kSets];
-        float4 acc[RB];
+    for (int x = 0; x < kSets; ++x) m[x] = l[x] = 0.f, see[x] = 0;
+
+    // The warps joined, when a piece ends: maxima and sums meet in shared
+    // memory; each scales its output to the common maximum and leaves it in the
+    // stage, and each sums and writes some rows of its group.
+    auto finish = [&](float4* scratch) -> bool {
 #pragma unroll
         for (int x = 0; x < kSets; ++x) {
-            see[x] = visible(a, p.len, p.nq, (r0 + 4 * x + my_row) % a.n);
-            m[x] = -INFINITY;
-            l[x] = 0.f;
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
+            if (lane < 4) {
+                stat_m[warp][4 * x + lane] = m[x];
+                stat_l[warp][4 * x + lane] = l[x];
+            }
+        }
+        if constexpr (kVKeys == 2) {                       // the two keys' halves of the output
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                acc[r].x += __shfl_xor_sync(0xffffffffu, acc[r].x, 16);
+                acc[r].y += __shfl_xor_sync(0xffffffffu, acc[r].y, 16);
+                acc[r].z += __shfl_xor_sync(0xffffffffu, acc[r].z, 16);
+                acc[r].w += __shfl_xor_sync(0xffffffffu, acc[r].w, 16);
+            }
+        }
+        constexpr int kGroup = C::kKeyWarps, kChunks = DV / 4;
+        const int w0 = group * kGroup;
+        warp_arrive(&ring.joint[0][0]);
+        if (!ring_wait(ring, &ring.joint[0][0], joints, budget_ns)) return false;
+        // Common maximum and sum of row `lane` (the first RB lanes), and what
+        // this warp's outputs are scaled with.
+        float M = -INFINITY, L = 0.f, f = 0.f;
+        if (lane < RB) {
+#pragma unroll
+            for (int x = 0; x < kGroup; ++x) M = fmaxf(M, stat_m[w0 + x][lane]);
+            const float z = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int x = 0; x < kGroup; ++x) L = fmaf(stat_l[w0 + x][lane], exp2f(stat_m[w0 + x][lane] - z), L);
+            f = exp2f(stat_m[warp][lane] - z);
         }
 #pragma unroll
-        for (int r = 0; r < RB; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int see_all = a.causal ? p.len - (p.nq - 1) : p.len;
+        for (int r = 0; r < RB; ++r) {
+            const float fr = __shfl_sync(0xffffffffu, f, r);
+            if (lane < kChunks)
+                scratch[(warp * RB + r) * kChunks + lane] =
+                    make_float4(acc[r].x * fr, acc[r].y * fr, acc[r].z * fr, acc[r].w * fr);
+        }
+        warp_arrive(&ring.joint[0][1]);
+        if (!ring_wait(ring, &ring.joint[0][1], joints, budget_ns)) return false;
+        joints ^= 1;
+        const bool all = (at.flags & (kStarts | kEnds)) == (kStarts | kEnds);
+        const size_t slot = (2 * size_t(blockIdx.x) + (at.flags & kStarts ? 1 : 0)) * C::kTileRows;
+        if (!all && warp == 0 && lane == 0) note_head(parts, at);
+        for (int r = kg; r < RB; r += kGroup) {
+            const int row = group * RB + r;
+            const float Mr = __shfl_sync(0xffffffffu, M, r), Lr = __shfl_sync(0xffffffffu, L, r);
+            if (row >= at.rows || (all && query_of(a, at, row) >= at.nq)) continue;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < kChunks) {
+#pragma unroll
+                for (int x = 0; x < kGroup; ++x) {
+                    const float4 y = scratch[((w0 + x) * RB + r) * kChunks + lane];
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                }
+            }
+            const size_t to = (all ? size_t(at.row) : slot) + row;
+            if (all) {
+                const float inv = Lr > 0.f ? 1.f / Lr : Lr == 0.f ? 0.f : Lr;            // NaN stays
+                if (4 * lane < a.dv)
+                    *reinterpret_cast<float4*>(O + to * a.dv + 4 * lane) =
+                        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                if (lane == 0) LSE[to] = (Mr + log2f(Lr)) * kLn2;
+            } else {
+                if (4 * lane < a.dv) *reinterpret_cast<float4*>(parts.o + to * a.dv + 4 * lane) = o;
+                if (lane == 0) *reinterpret_cast<float2*>(parts.ml + to * 2) = make_float2(Mr, Lr);
+            }
+        }
+        return true;
+    };
 
-        for (int t = p.t0; t < p.t1; ++t, ++n) {
-            const int s = n % kStages;
-            ring_wait(ring, &ring.full[s], (n / kStages) & 1, budget_ns);
+    uint32_t parity = 0;
+    for (int s = 0;; s = s + 1 == kStages ? 0 : s + 1, parity ^= s == 0) {
+        if (!ring_wait(ring, &ring.full[s], parity, budget_ns)) return;
+        const int flags = ring.stage[s].flags;
+        if (flags & kStop) return;
+        if (flags & kFirst) {
+            at = piece_at(ring, s);
+            const int len = ring.stage[s].len, r0 = group * RB;
+            // Query columns 4 (s16 + 16 x) of every row.
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+#pragma unroll
+                for (int x = 0; x < kQ; ++x) {
+                    const int c = 4 * (s16 + 16 * x);
+                    q[r][x] = r0 + r < at.rows && c < a.d
+                                  ? *reinterpret_cast<const float4*>(Q + (size_t(at.row) + r0 + r) * a.d + c)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+            see_all = a.causal ? len - (at.nq - 1) : len;
+            tile0 = ring.stage[s].t0 * kTileKeys;
+#pragma unroll
+            for (int x = 0; x < kSets; ++x) {
+                see[x] = visible(a, len, at.nq, query_of(a, at, r0 + 4 * x + my_row));
+                m[x] = -INFINITY;
+                l[x] = 0.f;
+            }
+#pragma unroll
+            for (int r = 0; r < RB; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        {
+            const bool rows_here = group * RB < at.rows;
             const uint8_t* st = smem + s * C::kStageBytes;
 #pragma unroll 1
             for (int k8 = kg * C::kWarpKeys; rows_here && k8 < (kg + 1) * C::kWarpKeys; k8 += 8) {
-                const uint32_t there = uint32_t(ring.present[s] >> k8) & 0xffu;
+                const uint32_t there = uint32_t(ring.stage[s].present >> k8) & 0xffu;
                 if (there == 0) continue;
                 // Scores of keys k8 + 2 pair + kp, partial over this lane's columns.
                 float part[kSets][16];
@@ -143,7 +230,7 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     }
                     sc[x] = part[x][0] * scale_log2;       // row 4 x + my_row, key k8 + my_key
                 }
-                const int k0 = t * kTileKeys + k8;
+                const int k0 = tile0 + k8;
                 const bool whole = there == 0xffu && k0 + 8 <= see_all;
                 if (!whole) {
 #pragma unroll
@@ -210,106 +297,14 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 }
                 __syncwarp();                              // weights are read before the next 8 keys'
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ring.empty[s]);
         }
-
-        // ------------------------------------------ the group's warps joined
-#pragma unroll
-        for (int x = 0; x < kSets; ++x) {
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
-            if (lane < 4) {
-                stat_m[warp][4 * x + lane] = m[x];
-                stat_l[warp][4 * x + lane] = l[x];
-            }
+        tile0 += kTileKeys;
+        if (flags & kLast) {
+            // Every warp has read the stage once they have met.
+            if (!finish(reinterpret_cast<float4*>(smem + s * C::kStageBytes))) return;
+            fence_proxy_async_smem();                      // before the TMA writes there again
         }
-        if constexpr (kVKeys == 2) {                       // the two keys' halves of the output
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                acc[r].x += __shfl_xor_sync(0xffffffffu, acc[r].x, 16);
-                acc[r].y += __shfl_xor_sync(0xffffffffu, acc[r].y, 16);
-                acc[r].z += __shfl_xor_sync(0xffffffffu, acc[r].z, 16);
-                acc[r].w += __shfl_xor_sync(0xffffffffu, acc[r].w, 16);
-            }
-        }
-        constexpr int kGroup = C::kKeyWarps;               // warps that are joined, ids 1 + group
-        const int w0 = group * kGroup, bar = R == 1 ? 1 : 1 + group;
-        auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(kGroup * 32) : "memory"); };
-        meet();
-        float M[RB], L[RB];
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            M[r] = -INFINITY;
-            L[r] = 0.f;
-            for (int x = 0; x < kGroup; ++x) M[r] = fmaxf(M[r], stat_m[w0 + x][r]);
-            const float z = M[r] == -INFINITY ? 0.f : M[r];
-            for (int x = 0; x < kGroup; ++x) L[r] = fmaf(stat_l[w0 + x][r], exp2f(stat_m[w0 + x][r] - z), L[r]);
-            const float f = exp2f(stat_m[warp][r] - z);
-            acc[r].x *= f;
-            acc[r].y *= f;
-            acc[r].z *= f;
-            acc[r].w *= f;
-        }
-        // The upper half of the warps leaves its outputs, the lower half adds its
-        // own and leaves the sums, and every warp takes some rows of their sum.
-        constexpr int kHalf = kGroup / 2, kChunks = DV / 4;
-        float4* mine = joined + (group * kHalf + kg % kHalf) * (RB * kChunks);
-        if (kg >= kHalf && lane < kChunks) {
-#pragma unroll
-            for (int r = 0; r < RB; ++r) mine[r * kChunks + lane] = acc[r];
-        }
-        meet();
-        if (kg < kHalf && lane < kChunks) {
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const float4 o = mine[r * kChunks + lane];
-                mine[r * kChunks + lane] = make_float4(acc[r].x + o.x, acc[r].y + o.y, acc[r].z + o.z, acc[r].w + o.w);
-            }
-        }
-        meet();
-        const bool all = p.t0 == 0 && p.t1 == p.tiles;
-        const size_t slot = 2 * size_t(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            const int row = r0 + r;
-            if (r % kGroup != kg || row >= a.rows) continue;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (lane < kChunks) {
-#pragma unroll
-                for (int x = 0; x < kHalf; ++x) {
-                    const float4 y = joined[((group * kHalf + x) * RB + r) * kChunks + lane];
-                    o.x += y.x;
-                    o.y += y.y;
-                    o.z += y.z;
-                    o.w += y.w;
-                }
-            }
-            if (all) {
-                if (row % a.n >= p.nq) continue;
-                const float inv = L[r] > 0.f ? 1.f / L[r] : L[r] == 0.f ? 0.f : L[r];    // NaN stays
-                if (4 * lane < a.dv)
-                    *reinterpret_cast<float4*>(O + (base + row) * a.dv + 4 * lane) =
-                        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                if (lane == 0) LSE[base + row] = (M[r] + log2f(L[r])) * kLn2;
-            } else {
-                const size_t at = slot * C::kTileRows + group * RB + r;
-                if (4 * lane < a.dv) *reinterpret_cast<float4*>(parts.o + at * a.dv + 4 * lane) = o;
-                if (lane == 0) {
-                    parts.ml[at * 2] = M[r];
-                    parts.ml[at * 2 + 1] = L[r];
-                }
-            }
-        }
-        if (!all && p.t0 == 0 && warp == 0 && lane == 0) {
-            Head h;
-            h.b = p.b;
-            h.item = p.item;
-            h.nq = p.nq;
-            h.last = w.owner(p.end - 1);
-            parts.head[blockIdx.x] = h;
-        }
-        meet();                                            // sums and statistics are read
+        warp_arrive(&ring.empty[s]);
     }
 }
 

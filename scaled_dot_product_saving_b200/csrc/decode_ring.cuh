@@ -3,7 +3,12 @@
 // one warp that runs ahead of the others, across the borders of pieces.
 //
 // A stage is panels of 64 rows of 128 bytes (64 bf16 or 32 fp32 columns) in the
-// TMA's 128-byte swizzle: the K panels, then the V panels.
+// TMA's 128-byte swizzle: the K panels, then the V panels. The producer alone
+// knows the split of the call; it leaves beside each stage what the consumers
+// need: which keys are there, and with the first tile of a piece the piece.
+//
+// Every wait is bounded and on an mbarrier. One that runs out sets the abort
+// flag, which ends every other wait, and each warp leaves its loop.
 #pragma once
 
 #include "decode.cuh"
@@ -13,33 +18,50 @@ namespace paged {
 
 constexpr int kPanelBytes = kTileKeys * 128;
 
-template <int kStages>
+enum : int { kFirst = 1, kLast = 2, kStop = 4, kStarts = 8, kEnds = 16 };
+
+struct Stage {
+    unsigned long long present;      // keys of the tile that exist
+    int flags;                       // kFirst, kLast: tile of its piece; kStop: no tile, the end;
+                                     // kStarts, kEnds: the piece of its item
+    // with kFirst
+    int row, rows;                   // first query row of the item in Q, O and LSE, and how many
+    int i0;                          // the first row's query
+    int len, nq, t0;
+    int b, item, last;               // for the item's head: last, CTA of its last piece
+};
+
+template <int kStages, int kGroups>
 struct Ring {
     uint64_t full[kStages], empty[kStages];
-    unsigned long long present[kStages];           // keys of the stage that exist
+    uint64_t joint[kGroups][2];      // where the warps of a group meet when a piece ends
+    Stage stage[kStages];
     int abort;
 };
 
-// A wait that runs out sets the abort flag, after which every wait returns at
-// once: each role goes through its loops without data, so that no thread stays
-// behind at a barrier, and the error word tells the host.
-template <int kStages>
-__device__ __forceinline__ void ring_wait(Ring<kStages>& ring, uint64_t* bar, uint32_t parity,
-                                          unsigned long long budget_ns) {
+// False once the call is being abandoned.
+template <typename RingT>
+__device__ __forceinline__ bool ring_wait(RingT& ring, uint64_t* bar, uint32_t parity, unsigned long long budget_ns) {
     volatile int* abort = &ring.abort;
-    if (!mbar_wait(bar, parity, abort, budget_ns)) {
+    if (mbar_wait_warp(bar, parity, abort, budget_ns)) return true;
+    if (*abort == 0) {
         record_device_error(kErrTimeout);
         *abort = 1;
     }
+    return false;
 }
 
-// Collective over the block: barriers, the CTA's share of the work, and no head
-// yet. False (for all threads) if an earlier kernel's timeout has not been
-// read, in which case the call does nothing.
-template <int kStages>
-__device__ __forceinline__ bool set_up(const DecodeArgs& a, const Parts& parts, Ring<kStages>& ring,
-                                       const uint8_t* smem, int consumers, long long* scratch, long long* found,
-                                       Walker* w) {
+// One lane arrives for the warp, after all of it.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Collective over the block. False (for all threads) if an earlier kernel's
+// timeout has not been read, in which case the call does nothing.
+template <int kStages, int kGroups>
+__device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups>& ring, const uint8_t* smem,
+                                       int consumers) {
     if (threadIdx.x == 0) {
         parts.head[blockIdx.x].b = -1;
         const bool misaligned = (smem_addr(smem) & 1023u) != 0;
@@ -49,9 +71,13 @@ __device__ __forceinline__ bool set_up(const DecodeArgs& a, const Parts& parts, 
             mbar_init(&ring.full[s], 1);
             mbar_init(&ring.empty[s], consumers);
         }
+        for (int x = 0; x < kGroups; ++x) {
+            mbar_init(&ring.joint[x][0], consumers / kGroups);
+            mbar_init(&ring.joint[x][1], consumers / kGroups);
+        }
         fence_mbar_init();
     }
-    w->start(a, scratch, found);                    // ends with a barrier
+    __syncthreads();
     const bool skip = ring.abort != 0;
     __syncthreads();                                // every thread has read the flag
     grid_launch_dependents();                       // the join may set up meanwhile
@@ -61,26 +87,32 @@ __device__ __forceinline__ bool set_up(const DecodeArgs& a, const Parts& parts, 
 // The producer warp. A tile is 64 / box pages (box = min(page, 64) tokens, one
 // lane each); 32 table entries are held across the warp and the next 32 are on
 // the way. C: the kernel's configuration.
-template <typename C, int kStages>
+template <typename C, typename T, typename RingT>
 __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMap* tmV, const DecodeArgs& a,
-                                        Walker w, Ring<kStages>& ring, uint8_t* smem,
+                                        const T* Q, Walker& w, RingT& ring, uint8_t* smem,
                                         unsigned long long budget_ns) {
+    constexpr int kStages = C::kStages;
     const int lane = threadIdx.x & 31;
     const int page_log2 = a.g.page_log2, page = 1 << page_log2;
     const int box_log2 = min(page_log2, 6), box = 1 << box_log2, boxes = kTileKeys >> box_log2;
-    if (lane == 0) {
-        prefetch_tensor_map(tmK);
-        prefetch_tensor_map(tmV);
-    }
-    int n = 0;                                      // tiles issued
+    int n = 0, s = 0;                               // tiles issued, stage of the next
+    uint32_t parity = 1;                            // of the empty barriers: the first round passes
+    bool going = true;
     Piece p;
-    while (w.next(a, &p)) {
-        const int hk = p.item / a.row_tiles;
+    while (going && w.next(a, &p)) {
+        const int hk = a.row_tiles == 1 ? p.item : p.item / a.row_tiles;
+        const int r0 = (p.item - hk * a.row_tiles) * a.tile_rows, rows = min(a.tile_rows, a.rows - r0);
+        const int q_row = int(row_base(a, p.b, hk)) + r0;
+        // The query rows, into L1 ahead of the warps that will read them.
+        const char* q = reinterpret_cast<const char*>(Q + size_t(q_row) * a.d);
+        for (int x = lane * 128; x < rows * a.d * int(sizeof(T)); x += 32 * 128)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
         const int* row = a.table + size_t(p.b) * a.g.M;
         const int last = pages_of(p.len, page_log2);
         int base = (p.t0 * kTileKeys) >> page_log2;
         int held = base + lane < last ? row[base + lane] : -1;
         int ahead = base + 32 + lane < last ? row[base + 32 + lane] : -1;
+        const int last_cta = p.t0 == 0 && p.t1 < p.tiles ? w.owner(p.end - 1) : 0;
         for (int t = p.t0; t < p.t1; ++t, ++n) {
             const int k0 = t * kTileKeys, first = k0 >> page_log2;
             if (first - base >= 32) {
@@ -92,9 +124,10 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
             const int entry = __shfl_sync(0xffffffffu, held, (key >> page_log2) - base);
             const bool load = lane < boxes && key < p.len && page_ok(entry, a.g.P);
             const unsigned loads = __ballot_sync(0xffffffffu, load);
-            const int s = n % kStages;
-            if (n >= kStages) ring_wait(ring, &ring.empty[s], (n / kStages - 1) & 1, budget_ns);
-            const bool go = __all_sync(0xffffffffu, !*reinterpret_cast<volatile int*>(&ring.abort));
+            if (!ring_wait(ring, &ring.empty[s], parity, budget_ns)) {
+                going = false;
+                break;
+            }
             if (lane == 0) {
                 unsigned long long keys = ~0ull;
                 if (loads != (1u << boxes) - 1u) {
@@ -104,11 +137,26 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                         if (loads >> x & 1) keys |= one << (x << box_log2);
                 }
                 if (p.len - k0 < kTileKeys) keys &= p.len > k0 ? (1ull << (p.len - k0)) - 1ull : 0ull;
-                ring.present[s] = keys;
-                mbar_arrive_expect_tx(&ring.full[s], go ? __popc(loads) * box * (C::kKPanels + C::kVPanels) * 128 : 0);
+                Stage& st = ring.stage[s];
+                st.present = keys;
+                int flags = t == p.t1 - 1 ? kLast : 0;
+                if (t == p.t0) {
+                    flags |= kFirst | (p.t0 == 0 ? kStarts : 0) | (p.t1 == p.tiles ? kEnds : 0);
+                    st.row = q_row;
+                    st.rows = rows;
+                    st.i0 = a.n == 1 ? 0 : r0 % a.n;
+                    st.len = p.len;
+                    st.nq = p.nq;
+                    st.t0 = p.t0;
+                    st.b = p.b;
+                    st.item = p.item;
+                    st.last = last_cta;
+                }
+                st.flags = flags;
+                mbar_arrive_expect_tx(&ring.full[s], __popc(loads) * box * (C::kKPanels + C::kVPanels) * 128);
             }
             __syncwarp();
-            if (load && go) {
+            if (load) {
                 uint8_t* dst = smem + s * C::kStageBytes + (lane << box_log2) * 128;
                 const int z = entry * a.g.Hkv + hk, y = key & (page - 1);
 #pragma unroll
@@ -118,11 +166,40 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                 for (int x = 0; x < C::kVPanels; ++x)
                     tma_load_3d(dst + C::kKBytes + x * kPanelBytes, tmV, &ring.full[s], C::kPanelCols * x, y, z);
             }
+            if (++s == kStages) {
+                s = 0;
+                parity ^= 1;
+            }
         }
     }
-    // No copy may be in flight into shared memory that the CTA gives back.
-    for (int x = max(0, n - kStages); x < n; ++x)
+    const bool stopped = going && ring_wait(ring, &ring.empty[s], parity, budget_ns);
+    if (stopped && lane == 0) {
+        ring.stage[s].flags = kStop;
+        mbar_arrive(&ring.full[s]);
+    }
+    // No copy may be in flight into shared memory that the CTA gives back. (The
+    // stage that the end took was empty, and its barrier has moved on.)
+    for (int x = max(0, n - kStages + (stopped ? 1 : 0)); x < n; ++x)
         (void)mbar_wait_timed(&ring.full[x % kStages], (x / kStages) & 1, budget_ns);
+}
+
+// What a consumer keeps of the piece it is at.
+struct At {
+    int row, rows, i0, nq, flags;
+    int b, item, last;
+};
+template <typename RingT>
+__device__ __forceinline__ At piece_at(const RingT& ring, int s) {
+    const Stage& st = ring.stage[s];
+    return At{st.row, st.rows, st.i0, st.nq, st.flags, st.b, st.item, st.last};
+}
+// The query that row r of the item belongs to.
+__device__ __forceinline__ int query_of(const DecodeArgs& a, const At& at, int r) {
+    return a.n == 1 ? 0 : (at.i0 + r) % a.n;
+}
+__device__ __forceinline__ void note_head(const Parts& parts, const At& at) {
+    if ((at.flags & (kStarts | kEnds)) == kStarts)
+        parts.head[blockIdx.x] = Head{at.b, at.item, at.last, at.nq};
 }
 
 }  // namespace paged

@@ -36,16 +36,14 @@ struct DecodeCfg {
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
     static constexpr int kThreads = (kKeyWarps * R + 1) * 32;
-    // Two CTAs an SM for 16 rows (96 KB of stages each), one for more.
+    // Outputs of a group's four warps, when a piece ends: with one group in the
+    // stage of the piece's last tile, if they fit, else beside the stages.
+    static constexpr int kScratchBytes = kKeyWarps * 16 * DV * 4;
+    static constexpr bool kInStage = R == 1 && kScratchBytes <= kStageBytes;
+    // Two CTAs an SM for 16 rows (113 KB each), one for 32.
     static constexpr int kCtasPerSm = R == 1 ? 2 : 1;
-    static constexpr int kStages = (R == 1 ? 96 : 160) * 1024 / kStageBytes;
-    static constexpr int kJoinBytes = R * 16 * DV * 4;
-    // With four groups a thread has 96 registers: query fragments are read from
-    // shared memory at every use instead of being held.
-    static constexpr bool kQShared = R == 4;
-    static constexpr int kQPitch = DK * 2 + 16;
-    static constexpr int kOffQ = kStages * kStageBytes + kJoinBytes;
-    static constexpr int kSmemBytes = kOffQ + (kQShared ? R * 16 * kQPitch : 0);
+    static constexpr int kStages = (R == 2 ? 128 : kInStage ? 96 : 72) * 1024 / kStageBytes;
+    static constexpr int kSmemBytes = kStages * kStageBytes + (kInStage ? 0 : R * kScratchBytes);
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -67,9 +65,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void group_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 // Either half of a pair of bf16 infinite or NaN.
 __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -83,16 +78,15 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     using C = DecodeCfg<DK, DV, R>;
     constexpr int kTileRows = 16 * R, kStages = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long scratch[33], found[2];
-    __shared__ Ring<kStages> ring;
+    __shared__ Ring<kStages, R> ring;
     __shared__ float stat_m[R][kKeyWarps][16], stat_l[R][kKeyWarps][16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     Walker w;
-    if (!set_up(a, parts, ring, smem, kKeyWarps * R, scratch, found, &w)) return;
-
+    if (warp == kKeyWarps * R) w.start(a);                // while the barriers are set up
+    if (!set_up(parts, ring, smem, kKeyWarps * R)) return;
     if (warp == kKeyWarps * R) {
-        produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns);
+        produce<C>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns);
         return;
     }
 
@@ -100,7 +94,6 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     const int kg = warp % kKeyWarps, mt = warp / kKeyWarps;
     const int g = lane >> 2, t4 = lane & 3;
     const float scale_log2 = a.scale * 1.4426950408889634f;
-    float4* joined = reinterpret_cast<float4*>(smem + kStages * C::kStageBytes) + mt * (16 * DV / 4);
     // ldmatrix rows of this lane: K by (key half, 8-dim half) = (bit 4, bit 3)
     // of the lane, V by (8-dim half, key half).
     const uint32_t sm = smem_addr(smem);
@@ -109,61 +102,134 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     const uint32_t v_row = C::kKBytes + (kg * 16 + (((lane >> 3) & 1) << 3) + (lane & 7)) * 128;
     const uint32_t v_x = ((lane >> 4) ^ (lane & 7)) << 4;
 
-    int n = 0;
-    Piece p;
-    while (w.next(a, &p)) {
-        const int hk = p.item / a.row_tiles, r0 = (p.item % a.row_tiles) * kTileRows + mt * 16;
-        const size_t base = row_base(a, p.b, hk);
-        const bool rows_here = r0 < a.rows;               // else only the barriers
-        // Query rows as A fragments: rows g and g + 8, widths past d as zeros.
-        uint32_t qf[C::kQShared ? 1 : DK / 16][4];
-        const uint32_t q_at = sm + C::kOffQ + (mt * 16 + (lane & 15)) * C::kQPitch + (lane >> 4) * 16;
-        if constexpr (C::kQShared) {
-            group_sync(1 + mt, kKeyWarps * 32);           // the last piece's are read
-            for (int x = kg * 32 + lane; x < 16 * (DK / 2); x += kKeyWarps * 32) {
-                const int r = x / (DK / 2), c = x % (DK / 2) * 2;
-                *reinterpret_cast<uint32_t*>(smem + C::kOffQ + (mt * 16 + r) * C::kQPitch + c * 2) =
-                    r0 + r < a.rows && c < a.d ? *reinterpret_cast<const uint32_t*>(Q + (base + r0 + r) * a.d + c)
-                                               : 0u;
+    At at{};
+    uint32_t joints = 0;                                  // parity of the group's next meeting
+    uint32_t qf[DK / 16][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float acc[DV / 8][4];
+    int see0 = 0, see1 = 0, see_all = 0, k0 = 0;
+
+    // The four warps of the group joined, when a piece ends: their maxima and
+    // sums meet in shared memory; each scales its output to the common maximum
+    // and leaves it there, and each sums and writes a quarter of the columns.
+    auto finish = [&](uint8_t* scratch) -> bool {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        if (t4 == 0) {
+            stat_m[mt][kg][g] = m0;
+            stat_m[mt][kg][g + 8] = m1;
+            stat_l[mt][kg][g] = l0;
+            stat_l[mt][kg][g + 8] = l1;
+        }
+        warp_arrive(&ring.joint[mt][0]);
+        if (!ring_wait(ring, &ring.joint[mt][0], joints, budget_ns)) return false;
+        float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < kKeyWarps; ++x) {
+            M0 = fmaxf(M0, stat_m[mt][x][g]);
+            M1 = fmaxf(M1, stat_m[mt][x][g + 8]);
+        }
+        const float Z0 = M0 == -INFINITY ? 0.f : M0, Z1 = M1 == -INFINITY ? 0.f : M1;
+        const float f0 = ex2(m0 - Z0), f1 = ex2(m1 - Z1);
+        float4* out = reinterpret_cast<float4*>(scratch) + lane;
+#pragma unroll
+        for (int x = 0; x < DV / 8; ++x)
+            out[(kg * (DV / 8) + x) * 32] = make_float4(acc[x][0] * f0, acc[x][1] * f0, acc[x][2] * f1, acc[x][3] * f1);
+#pragma unroll
+        for (int x = 0; x < kKeyWarps; ++x) {
+            L0 = fmaf(stat_l[mt][x][g], ex2(stat_m[mt][x][g] - Z0), L0);
+            L1 = fmaf(stat_l[mt][x][g + 8], ex2(stat_m[mt][x][g + 8] - Z1), L1);
+        }
+        warp_arrive(&ring.joint[mt][1]);
+        const bool all = (at.flags & (kStarts | kEnds)) == (kStarts | kEnds);
+        const int ra = mt * 16 + g, rb = ra + 8;
+        const bool put0 = ra < at.rows && (!all || query_of(a, at, ra) < at.nq);
+        const bool put1 = rb < at.rows && (!all || query_of(a, at, rb) < at.nq);
+        const float inv0 = all ? (L0 > 0.f ? 1.f / L0 : L0 == 0.f ? 0.f : L0) : 1.f;         // NaN stays
+        const float inv1 = all ? (L1 > 0.f ? 1.f / L1 : L1 == 0.f ? 0.f : L1) : 1.f;
+        const size_t slot = (2 * size_t(blockIdx.x) + (at.flags & kStarts ? 1 : 0)) * kTileRows;
+        const size_t to0 = (all ? size_t(at.row) : slot) + ra, to1 = to0 + 8;
+        if (kg == 0 && t4 == 0) {
+            if (all) {
+                if (put0) LSE[to0] = (M0 + log2f(L0)) * kLn2;
+                if (put1) LSE[to1] = (M1 + log2f(L1)) * kLn2;
+            } else {
+                if (put0) *reinterpret_cast<float2*>(parts.ml + to0 * 2) = make_float2(M0, L0);
+                if (put1) *reinterpret_cast<float2*>(parts.ml + to1 * 2) = make_float2(M1, L1);
+                if (mt == 0 && lane == 0) note_head(parts, at);
             }
-            group_sync(1 + mt, kKeyWarps * 32);
-        } else {
+        }
+        if (!ring_wait(ring, &ring.joint[mt][1], joints, budget_ns)) return false;
+        joints ^= 1;
+        constexpr int kCols = DV / 8 / kKeyWarps;         // blocks of 8 columns a warp
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+            const int c8 = kg * kCols + x, c = 8 * c8 + 2 * t4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kKeyWarps; ++k) {
+                const float4 o = out[(k * (DV / 8) + c8) * 32];
+                y.x += o.x;
+                y.y += o.y;
+                y.z += o.z;
+                y.w += o.w;
+            }
+            if (c >= a.dv) continue;
+            if (all) {
+                if (put0) *reinterpret_cast<uint32_t*>(O + to0 * a.dv + c) = pack_bf16x2(y.x * inv0, y.y * inv0);
+                if (put1) *reinterpret_cast<uint32_t*>(O + to1 * a.dv + c) = pack_bf16x2(y.z * inv1, y.w * inv1);
+            } else {
+                if (put0) *reinterpret_cast<float2*>(parts.o + to0 * a.dv + c) = make_float2(y.x, y.y);
+                if (put1) *reinterpret_cast<float2*>(parts.o + to1 * a.dv + c) = make_float2(y.z, y.w);
+            }
+        }
+        return true;
+    };
+
+    uint32_t parity = 0;
+    for (int s = 0;; s = s + 1 == kStages ? 0 : s + 1, parity ^= s == 0) {
+        if (!ring_wait(ring, &ring.full[s], parity, budget_ns)) return;
+        const int flags = ring.stage[s].flags;
+        if (flags & kStop) return;
+        if (flags & kFirst) {
+            at = piece_at(ring, s);
+            const int len = ring.stage[s].len, r = mt * 16 + g;
+            // Query rows g and g + 8 as A fragments, widths past d as zeros.
+            const __nv_bfloat16* q = Q + (size_t(at.row) + r) * a.d + 2 * t4;
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int r = r0 + g + (x & 1) * 8, c = ks * 16 + 2 * t4 + (x >> 1) * 8;
-                    qf[ks][x] = r < a.rows && c < a.d
-                                    ? *reinterpret_cast<const uint32_t*>(Q + (base + r) * a.d + c)
+                    const int c = ks * 16 + (x >> 1) * 8;
+                    qf[ks][x] = r + (x & 1) * 8 < at.rows && c < a.d
+                                    ? *reinterpret_cast<const uint32_t*>(q + (x & 1) * 8 * a.d + c)
                                     : 0u;
                 }
             }
-        }
-        // Keys that rows g and g + 8 see, and that every row sees.
-        const int see0 = visible(a, p.len, p.nq, (r0 + g) % a.n);
-        const int see1 = visible(a, p.len, p.nq, (r0 + g + 8) % a.n);
-        const int see_all = a.causal ? p.len - (p.nq - 1) : p.len;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        float acc[DV / 8][4];
+            // Keys that rows g and g + 8 see, and that every row sees.
+            see0 = visible(a, len, at.nq, query_of(a, at, r));
+            see1 = visible(a, len, at.nq, query_of(a, at, r + 8));
+            see_all = a.causal ? len - (at.nq - 1) : len;
+            k0 = ring.stage[s].t0 * kTileKeys + kg * 16;
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.f;
 #pragma unroll
-        for (int x = 0; x < DV / 8; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
-
-        for (int t = p.t0; t < p.t1; ++t, ++n) {
-            const int s = n % kStages;
-            ring_wait(ring, &ring.full[s], (n / kStages) & 1, budget_ns);
+            for (int x = 0; x < DV / 8; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+        }
+        {
+            const bool rows_here = mt * 16 < at.rows;     // else only the barriers
             const uint32_t st = sm + s * C::kStageBytes;
-            const int k0 = t * kTileKeys + kg * 16;       // this warp's keys
-            const uint32_t there = uint32_t(ring.present[s] >> (kg * 16)) & 0xffffu;
+            const uint32_t there = uint32_t(ring.stage[s].present >> (kg * 16)) & 0xffffu;
             if (rows_here && there != 0) {
                 float sc[2][4] = {};
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     uint32_t b[4];
                     ldsm4(st + (ks / 4) * kPanelBytes + k_row + (k_x ^ ((ks & 3) << 5)), b);
-                    uint32_t(&q)[4] = qf[C::kQShared ? 0 : ks];
-                    if constexpr (C::kQShared) ldsm4(q_at + ks * 32, q);
-                    mma16816(sc[0], q, b[0], b[1]);
-                    mma16816(sc[1], q, b[2], b[3]);
+                    mma16816(sc[0], qf[ks], b[0], b[1]);
+                    mma16816(sc[1], qf[ks], b[2], b[3]);
                 }
                 // sc[h][0..1]: row g, keys 8 h + 2 t4 + {0, 1}; sc[h][2..3]: row g + 8.
                 const bool whole = there == 0xffffu && k0 + 16 <= see_all;
@@ -280,104 +346,15 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ring.empty[s]);
         }
-
-        // ------------------------------------------- the four warps joined
-        // Their maxima and sums meet in shared memory; each scales its output
-        // to the common maximum, and they are added in the order of the warps.
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        if (t4 == 0) {
-            stat_m[mt][kg][g] = m0;
-            stat_m[mt][kg][g + 8] = m1;
-            stat_l[mt][kg][g] = l0;
-            stat_l[mt][kg][g + 8] = l1;
+        k0 += kTileKeys;
+        if (flags & kLast) {
+            // Every warp of the group has read the stage once they have met.
+            uint8_t* scratch = smem + (C::kInStage ? s * C::kStageBytes : kStages * C::kStageBytes + mt * C::kScratchBytes);
+            if (!finish(scratch)) return;
+            if (C::kInStage) fence_proxy_async_smem();    // before the TMA writes there again
         }
-        group_sync(R == 1 ? 1 : 1 + mt, kKeyWarps * 32);
-        float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
-#pragma unroll
-        for (int x = 0; x < kKeyWarps; ++x) {
-            M0 = fmaxf(M0, stat_m[mt][x][g]);
-            M1 = fmaxf(M1, stat_m[mt][x][g + 8]);
-        }
-        const float Z0 = M0 == -INFINITY ? 0.f : M0, Z1 = M1 == -INFINITY ? 0.f : M1;
-#pragma unroll
-        for (int x = 0; x < kKeyWarps; ++x) {
-            L0 = fmaf(stat_l[mt][x][g], ex2(stat_m[mt][x][g] - Z0), L0);
-            L1 = fmaf(stat_l[mt][x][g + 8], ex2(stat_m[mt][x][g + 8] - Z1), L1);
-        }
-        const float f0 = ex2(m0 - Z0), f1 = ex2(m1 - Z1);
-#pragma unroll
-        for (int x = 0; x < DV / 8; ++x) {
-            acc[x][0] *= f0;
-            acc[x][1] *= f0;
-            acc[x][2] *= f1;
-            acc[x][3] *= f1;
-        }
-#pragma unroll 1
-        for (int turn = kKeyWarps - 1; turn >= 0; --turn) {
-            if (kg == turn) {
-#pragma unroll
-                for (int x = 0; x < DV / 8; ++x) {
-                    if (turn < kKeyWarps - 1) {
-                        const float4 o = joined[x * 32 + lane];
-                        acc[x][0] += o.x;
-                        acc[x][1] += o.y;
-                        acc[x][2] += o.z;
-                        acc[x][3] += o.w;
-                    }
-                    if (turn > 0) joined[x * 32 + lane] = make_float4(acc[x][0], acc[x][1], acc[x][2], acc[x][3]);
-                }
-            }
-            if (turn > 0) group_sync(R == 1 ? 1 : 1 + mt, kKeyWarps * 32);
-        }
-        if (kg != 0) continue;
-
-        const bool all = p.t0 == 0 && p.t1 == p.tiles;
-        const size_t slot = 2 * size_t(blockIdx.x) + (p.t0 == 0 ? 1 : 0);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = r0 + g + 8 * half;
-            if (r >= a.rows) continue;
-            const float L = half ? L1 : L0, M = half ? M1 : M0;
-            if (all) {
-                if (r % a.n >= p.nq) continue;
-                const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;     // NaN stays
-                __nv_bfloat16* o = O + (base + r) * a.dv;
-#pragma unroll
-                for (int x = 0; x < DV / 8; ++x) {
-                    const int c = 8 * x + 2 * t4;
-                    if (c < a.dv)
-                        *reinterpret_cast<uint32_t*>(o + c) =
-                            pack_bf16x2(acc[x][2 * half] * inv, acc[x][2 * half + 1] * inv);
-                }
-                if (t4 == 0) LSE[base + r] = (M + log2f(L)) * kLn2;
-            } else {
-                const int rt = mt * 16 + g + 8 * half;                        // row of the slot
-                float* o = parts.o + (slot * kTileRows + rt) * a.dv;
-#pragma unroll
-                for (int x = 0; x < DV / 8; ++x) {
-                    const int c = 8 * x + 2 * t4;
-                    if (c < a.dv) *reinterpret_cast<float2*>(o + c) = make_float2(acc[x][2 * half], acc[x][2 * half + 1]);
-                }
-                if (t4 == 0) {
-                    parts.ml[(slot * kTileRows + rt) * 2] = M;
-                    parts.ml[(slot * kTileRows + rt) * 2 + 1] = L;
-                }
-            }
-        }
-        if (!all && p.t0 == 0 && mt == 0 && lane == 0) {
-            Head h;
-            h.b = p.b;
-            h.item = p.item;
-            h.nq = p.nq;
-            h.last = w.owner(p.end - 1);
-            parts.head[blockIdx.x] = h;
-        }
+        warp_arrive(&ring.empty[s]);
     }
 }
 

@@ -62,15 +62,18 @@ __device__ __forceinline__ T block_exclusive(T v, T* scratch, T* total) {
 }
 
 // ------------------------------------------------- the split of a decode call
-// A call's work is counted in units: one key tile (kTileKeys keys) of one item
-// (sequence, key head, tile of query rows). A sequence with queries and no
-// keys counts one unit per item, so that its rows are written. Units are
-// numbered sequence by sequence, item by item, tile by tile, and CTA c of G
-// takes [total * c / G, total * (c + 1) / G): every CTA gets the same number
-// of tiles however the lengths are spread, which the host does not know. An
-// item cut by a CTA border is joined afterwards from its pieces.
+// A call's work is counted in units. An item (sequence, key head, tile of query
+// rows) costs one per key tile (kTileKeys keys) and kItemUnits for its start
+// and end. A sequence with queries and no keys has one (empty) tile per item,
+// so that its rows are written. Units are numbered sequence by sequence, item
+// by item, and every CTA takes the same number of consecutive ones, however
+// the lengths are spread, which the host does not know. An item cut by a CTA
+// border is joined afterwards from its pieces.
 constexpr int kTileKeys = 64;
-constexpr int kMinUnits = 1;
+#ifndef ITEM_UNITS
+#define ITEM_UNITS 2
+#endif
+constexpr int kItemUnits = ITEM_UNITS;
 
 struct DecodeArgs {
     Geometry g;
@@ -97,80 +100,100 @@ __device__ __forceinline__ int queries_of(const DecodeArgs& a, int b) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTileKeys - 1) / kTileKeys); }
 
-// The CTA's share: walks its pieces in order. Every thread of the block holds
-// the same walker.
+// x / y for x >= 0, y > 0: mostly both fit 32 bits, where it is much cheaper.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+    if (((x | y) >> 32) == 0) return (unsigned)x / (unsigned)y;
+    return x / y;
+}
+
+// A CTA's share, walked by one warp (all lanes hold the same walker). With
+// total = q * ctas + r, the first r CTAs take q + 1 units and the others q.
 struct Walker {
-    int b;
+    int b, ctas;            // ctas: those that have work
     long long off;          // units of sequence b already passed
     long long left;         // units left to this CTA
-    long long pos, total;   // number of the next unit, and of all units
-    int ctas;               // CTAs that have work: each gets kMinUnits at least
+    long long pos;          // number of the next unit
+    long long q, r;
 
     static __device__ __forceinline__ long long units_of(const DecodeArgs& a, int b) {
         if (queries_of(a, b) <= 0) return 0;
-        return (long long)(a.g.Hkv * a.row_tiles) * tiles_of(clamp_len(__ldg(a.lens + b), a.g));
+        return (long long)(a.g.Hkv * a.row_tiles) * (tiles_of(clamp_len(__ldg(a.lens + b), a.g)) + kItemUnits);
     }
 
-    // Collective over the block. scratch: 33 values; found: 2 values.
-    __device__ void start(const DecodeArgs& a, long long* scratch, long long* found) {
-        const int chunk = (a.g.B + int(blockDim.x) - 1) / int(blockDim.x);
-        const int b0 = int(min((long long)a.g.B, (long long)threadIdx.x * chunk));
-        const int b1 = min(a.g.B, b0 + chunk);
+    __device__ void start(const DecodeArgs& a) {
+        const int lane = threadIdx.x & 31, chunk = (a.g.B + 31) / 32;
+        const int b0 = int(min((long long)a.g.B, (long long)lane * chunk)), b1 = min(a.g.B, b0 + chunk);
         long long sum = 0;
+#pragma unroll 4
         for (int k = b0; k < b1; ++k) sum += units_of(a, k);
-        const long long before = block_exclusive(sum, scratch, &total);
-        ctas = int(min((long long)gridDim.x, max(1ll, total / kMinUnits)));
-        const long long c = min((int)blockIdx.x, ctas);
-        pos = total * c / ctas;
-        left = total * min(c + 1, (long long)ctas) / ctas - pos;
-        if (left > 0 && pos >= before && pos < before + sum) {
-            long long x = before;
-            int k = b0;
-            for (;; ++k) {
-                const long long u = units_of(a, k);
+        long long inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        const long long total = __shfl_sync(0xffffffffu, inc, 31), before = inc - sum;
+        ctas = int(min((long long)gridDim.x, max(1ll, total)));
+        q = divide(total, ctas);
+        r = total - q * ctas;
+        const long long c = blockIdx.x;
+        left = c < ctas ? q + (c < r ? 1 : 0) : 0;
+        pos = q * c + min(c, r);
+        // The lane whose sequences hold unit pos looks for the sequence.
+        const bool mine = left > 0 && pos >= before && pos < inc;
+        int found = 0;
+        long long x = before;
+        if (mine) {
+            for (found = b0;; ++found) {
+                const long long u = units_of(a, found);
                 if (pos < x + u) break;
                 x += u;
             }
-            found[0] = k;
-            found[1] = pos - x;
         }
-        __syncthreads();
-        if (left > 0) {
-            b = int(found[0]);
-            off = found[1];
-        }
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        const int from = who ? __ffs(who) - 1 : 0;
+        b = __shfl_sync(0xffffffffu, found, from);
+        off = pos - __shfl_sync(0xffffffffu, x, from);
     }
 
     __device__ bool next(const DecodeArgs& a, Piece* p) {
-        if (left <= 0) return false;
         const int items = a.g.Hkv * a.row_tiles;
-        for (;; ++b, off = 0) {
-            p->nq = queries_of(a, b);
-            if (p->nq <= 0) continue;
-            p->len = clamp_len(__ldg(a.lens + b), a.g);
-            p->tiles = tiles_of(p->len);
-            if (off < (long long)items * p->tiles) break;
+        while (left > 0) {
+            for (;; ++b, off = 0) {
+                p->nq = queries_of(a, b);
+                if (p->nq <= 0) continue;
+                p->len = clamp_len(__ldg(a.lens + b), a.g);
+                p->tiles = tiles_of(p->len);
+                if (off < (long long)items * (p->tiles + kItemUnits)) break;
+            }
+            const int cost = p->tiles + kItemUnits;
+            p->b = b;
+            p->item = int(divide(off, cost));
+            const int at = int(off - (long long)p->item * cost);
+            const int used = int(min((long long)(cost - at), left));
+            p->t0 = max(0, at - kItemUnits);
+            p->t1 = max(0, at + used - kItemUnits);
+            p->end = pos - at + cost;
+            off += used;
+            pos += used;
+            left -= used;
+            if (p->t0 < p->t1) return true;
         }
-        p->b = b;
-        p->item = int(off / p->tiles);
-        p->t0 = int(off - (long long)p->item * p->tiles);
-        p->t1 = int(min((long long)p->tiles, p->t0 + left));
-        p->end = pos - p->t0 + p->tiles;
-        const int used = p->t1 - p->t0;
-        off += used;
-        pos += used;
-        left -= used;
-        return true;
+        return false;
     }
 
-    // The CTA that takes unit x: the largest c with total * c / ctas <= x.
-    __device__ int owner(long long x) const { return int(((x + 1) * ctas - 1) / total); }
+    // The CTA that takes unit x.
+    __device__ int owner(long long x) const {
+        const long long longer = r * (q + 1);
+        return int(x < longer ? divide(x, q + 1) : r + divide(x - longer, q));
+    }
 };
 
 // Pieces of cut items go through the workspace: CTA c writes its piece that
 // starts its item to slot 2c + 1, one that continues an earlier CTA's item to
 // slot 2c (it has at most one of each). head[c] describes the item that starts
-// in CTA c and goes on in later ones.
+// in CTA c and goes on in later ones. Between the first and the last CTA of an
+// item every CTA holds a piece of it.
 struct Head {
     int b;                  // -1: none
     int item;

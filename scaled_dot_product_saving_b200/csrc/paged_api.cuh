@@ -7,9 +7,9 @@ namespace {
 
 namespace pg = attn::paged;
 
-// Most CTAs of a decode call, and most CTAs times query rows of an item (64 rows
+// Most CTAs of a decode call, and most CTAs times query rows of an item (32 rows
 // on one CTA an SM; 16 rows on two): what the workspace has slots for.
-constexpr int kDecodeCtas = 2 * 148, kDecodeRows = 64 * 148;
+constexpr int kDecodeCtas = 2 * 148, kDecodeRows = 32 * 148;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -118,10 +118,15 @@ attn_status_t decode_simt(const pg::DecodeArgs& a, const void* Q, const void* Kp
 template <typename T>
 attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg::Parts& parts, int grid,
                           cudaStream_t st) {
+    // Warps per row: an item of few rows may come in many pieces (one key head,
+    // a long sequence), and few rows leave room for them.
     constexpr int kWarps = pg::kJoinThreads / 32;
-    const dim3 blocks(grid, (std::min(a.rows, a.tile_rows) + kWarps - 1) / kWarps);
+    const int rows = std::min(a.rows, a.tile_rows);
+    const int split = rows <= 4 ? 4 : rows <= 8 ? 2 : 1;
+    const dim3 blocks(grid, (rows * split + kWarps - 1) / kWarps);
     return traced(ATTN_KERNEL_DECODE_JOIN, st, [&] {
-        return launch_dependent(pg::decode_join<T>, blocks, pg::kJoinThreads, st, a, static_cast<T*>(O), LSE, parts)
+        return launch_dependent(pg::decode_join<T>, blocks, pg::kJoinThreads, st, a, static_cast<T*>(O), LSE, parts,
+                                split)
                    ? launched()
                    : ATTN_ERR_CUDA;
     });
@@ -169,7 +174,7 @@ attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const
                                    parts, grid, st);
 }
 
-// Query rows of an item: as many of a key head's as there are, up to 64 (bf16)
+// Query rows of an item: as many of a key head's as there are, up to 32 (bf16)
 // or 16 (fp32), since every item reads its keys again.
 template <int DK, int DV>
 attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
@@ -180,8 +185,7 @@ attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, cons
         return decode_f32<DK, DV, 8, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
     }
     if (a.rows <= 16) return decode_tc<DK, DV, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
-    if (a.rows <= 32) return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
-    return decode_tc<DK, DV, 4>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
 }
 
 // ------------------------------------------------------------------- books
@@ -280,7 +284,7 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     pg::DecodeArgs a{g, table, lens, q_len, H, n, d, dv, H / Hkv * n, pg::kRows, 0, causal != 0, scale};
     a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;      // the kernels' tiles may differ by a factor of 4
     // The kernel numbers its units (key tiles of all items) times CTAs in 64 bits.
-    if (4.0 * B * Hkv * a.row_tiles * ((static_cast<double>(max_pages) * page) / pg::kTileKeys + 1) >=
+    if (4.0 * B * Hkv * a.row_tiles * ((static_cast<double>(max_pages) * page) / pg::kTileKeys + 1 + pg::kItemUnits) >=
         9007199254740992.0)
         return ATTN_ERR_SHAPE;
     const size_t es = dtype == ATTN_F32 ? 4 : 2, rows = static_cast<size_t>(B) * H * n;
