@@ -248,103 +248,129 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const i
 // The copy kernels start while the books are still being written: what they
 // read of them they read from L2, after the wait.
 //
-// A warp takes spans of kSpan 16-byte units, four a lane in flight: the rows of
-// K of one (sequence, head), or of one head of a page, and then its rows of V;
-// widths wk, wv in units.
-constexpr int kCopyThreads = 256, kSpan = 128;
+// A warp takes a span at a time: up to kSpan 16-byte units (four a lane in
+// flight) of the rows of K, or of V, of one head of a sequence or page. Spans are
+// whole rows, so that where a lane's units lie in a row is the same in every
+// span, and the loop divides by multiplication: with 64-bit divisions the rows
+// of a large append were bound by instructions (37 us against 42 for 134 MB).
+constexpr int kCopyThreads = 256, kUnits = 4, kSpan = 32 * kUnits;
 
-__host__ __device__ constexpr unsigned long long spans_of(unsigned long long units) {
-    return (units + kSpan - 1) / kSpan;
-}
+// n / d for 0 <= n < 2^31.
+struct Divisor {
+    unsigned d, mul, shift;
+    static Divisor of(unsigned d) {
+        unsigned l = 0;
+        while (l < 31 && (1u << l) < d) ++l;
+        return Divisor{d, unsigned(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+    }
+    __device__ __forceinline__ unsigned divide(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+// Widths in 16-byte units, rows a span, and spans of a head's K and of its K and V.
+struct RowPlan {
+    int wk, wv, k_rows, v_rows;
+    unsigned k_spans;
+    Divisor spans, heads;
+    static RowPlan of(int wk, int wv, long long rows, int heads) {
+        RowPlan p{wk, wv, kSpan / wk, kSpan / wv, 0, {}, {}};
+        p.k_spans = unsigned((rows + p.k_rows - 1) / p.k_rows);
+        p.spans = Divisor::of(p.k_spans + unsigned((rows + p.v_rows - 1) / p.v_rows));
+        p.heads = Divisor::of(heads);
+        return p;
+    }
+};
 
 // New rows K [B, Hkv, n, wk], V [B, Hkv, n, wv] into their pages.
 __global__ void __launch_bounds__(kCopyThreads)
 append_rows(Geometry g, const uint4* __restrict__ K, const uint4* __restrict__ V, uint4* __restrict__ Kp,
             uint4* __restrict__ Vp, const int* table, const int* control, const int* start, const int* after,
-            int n, int wk, int wv) {
+            int n, RowPlan plan) {
     const int lane = threadIdx.x & 31, page = 1 << g.page_log2;
-    const unsigned long long k_spans = spans_of((unsigned long long)n * wk);
-    const unsigned long long spans = k_spans + spans_of((unsigned long long)n * wv), items = spans * g.B * g.Hkv;
-    const unsigned long long stride = (unsigned long long)gridDim.x * (kCopyThreads / 32);
-    // With one span a warp, its rows are on the way before the books are read;
-    // with more, rows that turn out to be padding are not worth reading.
-    const bool early = items <= stride;
+    const unsigned items = plan.spans.d * unsigned(g.B) * unsigned(g.Hkv), stride = gridDim.x * (kCopyThreads / 32);
+    // Of a small call (one token a sequence) the rows are on the way before the
+    // books are read; of a large one, rows that may be padding are not.
+    const bool early = items <= min(stride, 2048u);
     if (!early) {
         grid_dependency_wait();
         if (!__ldcg(control + kCtlMoves)) return;
     }
-    for (unsigned long long x = (unsigned long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items;
-         x += stride) {
-        const unsigned long long bh = x / spans;
-        unsigned long long span = x - bh * spans;
-        const int b = int(unsigned(bh) / unsigned(g.Hkv)), h = int(unsigned(bh) - unsigned(b) * g.Hkv);
-        const bool is_v = span >= k_spans;
-        if (is_v) span -= k_spans;
-        const unsigned w = is_v ? wv : wk;
-        // The span's first unit is column c0 of new row i0.
-        const unsigned i0 = unsigned(span * kSpan / w), c0 = unsigned(span * kSpan - (unsigned long long)i0 * w);
-        const uint4* from = (is_v ? V : K) + (bh * n + i0) * w;
+    // This lane's units of a span: row and column, in K's rows and in V's.
+    int ki[kUnits], kc[kUnits], vi[kUnits], vc[kUnits];
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+        const int u = lane + 32 * e;
+        ki[e] = u / plan.wk;
+        kc[e] = u - ki[e] * plan.wk;
+        if (ki[e] >= plan.k_rows) ki[e] = 0x3fffffff;
+        vi[e] = u / plan.wv;
+        vc[e] = u - vi[e] * plan.wv;
+        if (vi[e] >= plan.v_rows) vi[e] = 0x3fffffff;
+    }
+    for (unsigned x = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items; x += stride) {
+        const unsigned bh = plan.spans.divide(x), b = plan.heads.divide(bh), h = bh - b * plan.heads.d;
+        unsigned span = x - bh * plan.spans.d;
+        const bool is_v = span >= plan.k_spans;
+        if (is_v) span -= plan.k_spans;
+        const int w = is_v ? plan.wv : plan.wk;
+        const int i0 = int(span) * (is_v ? plan.v_rows : plan.k_rows);
+        const uint4* from = (is_v ? V : K) + (size_t(bh) * n + i0) * w + lane;
         uint4* pool = is_v ? Vp : Kp;
-        int t0 = 0;
-        unsigned add = n;
+        int t0 = 0, left = n - i0;                   // new rows from i0 on
         if (!early) {
             t0 = __ldcg(start + b);
-            add = __ldcg(after + b) - t0;
-            if (i0 >= add) continue;
+            left = __ldcg(after + b) - t0 - i0;
+            if (left <= 0) continue;
         }
-        uint4 v[4];
-        unsigned i[4], c[4];
+        uint4 v[kUnits];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const unsigned u = c0 + lane + 32 * e;
-            i[e] = i0 + u / w;
-            c[e] = u % w;
-            if (i[e] < add) v[e] = from[u];
-        }
+        for (int e = 0; e < kUnits; ++e)
+            if ((is_v ? vi[e] : ki[e]) < left) v[e] = __ldcs(from + 32 * e);
         if (early) {
             grid_dependency_wait();
             if (!__ldcg(control + kCtlMoves)) return;
             t0 = __ldcg(start + b);
-            add = __ldcg(after + b) - t0;
+            left = __ldcg(after + b) - t0 - i0;
         }
+        t0 += i0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (i[e] >= add) continue;
-            const int t = t0 + int(i[e]);
+        for (int e = 0; e < kUnits; ++e) {
+            const int i = is_v ? vi[e] : ki[e];
+            if (i >= left) continue;
+            const int t = t0 + i;
             const int p = __ldcg(table + size_t(b) * g.M + (t >> g.page_log2));
-            if (page_ok(p, g.P)) pool[((size_t(p) * g.Hkv + h) * page + (t & (page - 1))) * w + c[e]] = v[e];
+            if (page_ok(p, g.P))
+                pool[((size_t(p) * g.Hkv + h) * page + (t & (page - 1))) * w + (is_v ? vc[e] : kc[e])] = v[e];
         }
     }
 }
 
 // Rows [0, rows) of every head of the listed pages.
 __global__ void __launch_bounds__(kCopyThreads)
-move_rows(Geometry g, uint4* Kp, uint4* Vp, const int* control, const Move* moves, int wk, int wv) {
+move_rows(Geometry g, uint4* Kp, uint4* Vp, const int* control, const Move* moves, RowPlan plan) {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const unsigned k_spans = unsigned(spans_of((unsigned long long)wk << g.page_log2));
-    const unsigned spans = k_spans + unsigned(spans_of((unsigned long long)wv << g.page_log2));
-    const unsigned long long items = (unsigned long long)__ldcg(control + kCtlMoves) * g.Hkv * spans;
-    const unsigned long long stride = (unsigned long long)gridDim.x * (kCopyThreads / 32);
-    for (unsigned long long x = (unsigned long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items;
-         x += stride) {
-        const unsigned qh = unsigned(x / spans), q = qh / unsigned(g.Hkv), h = qh - q * g.Hkv;
-        unsigned span = unsigned(x - (unsigned long long)qh * spans);
-        const bool is_v = span >= k_spans;
-        if (is_v) span -= k_spans;
-        const unsigned w = is_v ? wv : wk;
+    // At most P / 2 pages of Hkv heads move: below 2^30 items of few spans each.
+    const unsigned long long items = (unsigned long long)__ldcg(control + kCtlMoves) * g.Hkv * plan.spans.d;
+    const unsigned stride = gridDim.x * (kCopyThreads / 32);
+    for (unsigned long long x = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items; x += stride) {
+        const unsigned qh = (x >> 31) == 0 ? plan.spans.divide(unsigned(x)) : unsigned(x / plan.spans.d);
+        const unsigned q = plan.heads.divide(qh), h = qh - q * plan.heads.d;
+        unsigned span = unsigned(x - (unsigned long long)qh * plan.spans.d);
+        const bool is_v = span >= plan.k_spans;
+        if (is_v) span -= plan.k_spans;
+        const int w = is_v ? plan.wv : plan.wk, rows = is_v ? plan.v_rows : plan.k_rows;
         const int4 m = __ldcg(reinterpret_cast<const int4*>(moves) + q);
-        const unsigned units = unsigned(m.z) * w, u0 = span * kSpan + lane;
+        const int units = min(rows, m.z - int(span) * rows) * w, u0 = int(span) * rows * w + lane;
         uint4* pool = is_v ? Vp : Kp;
-        const uint4* from = pool + ((size_t(m.x) * g.Hkv + h) << g.page_log2) * w;
-        uint4* to = pool + ((size_t(m.y) * g.Hkv + h) << g.page_log2) * w;
-        uint4 v[4];
+        const uint4* from = pool + ((size_t(m.x) * g.Hkv + h) << g.page_log2) * w + u0;
+        uint4* to = pool + ((size_t(m.y) * g.Hkv + h) << g.page_log2) * w + u0;
+        uint4 v[kUnits];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (u0 + 32 * e < units) v[e] = from[u0 + 32 * e];
+        for (int e = 0; e < kUnits; ++e)
+            if (lane + 32 * e < units) v[e] = __ldcs(from + 32 * e);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (u0 + 32 * e < units) to[u0 + 32 * e] = v[e];
+        for (int e = 0; e < kUnits; ++e)
+            if (lane + 32 * e < units) __stcs(to + 32 * e, v[e]);
     }
 }
 

@@ -95,6 +95,10 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
     const int lane = threadIdx.x & 31;
     const int page_log2 = a.g.page_log2, page = 1 << page_log2;
     const int box_log2 = min(page_log2, 6), box = 1 << box_log2, boxes = kTileKeys >> box_log2;
+    if (lane == 0) {
+        prefetch_tensor_map(tmK);
+        prefetch_tensor_map(tmV);
+    }
     int n = 0, s = 0;                               // tiles issued, stage of the next
     uint32_t parity = 1;                            // of the empty barriers: the first round passes
     bool going = true;

@@ -8,8 +8,8 @@ namespace {
 namespace pg = attn::paged;
 
 // Most CTAs of a decode call, and most CTAs times query rows of an item (32 rows
-// on one CTA an SM; 16 rows on two): what the workspace has slots for.
-constexpr int kDecodeCtas = 2 * 148, kDecodeRows = 32 * 148;
+// on one CTA an SM; 16 rows on up to three): what the workspace has slots for.
+constexpr int kDecodeCtas = 3 * 148, kDecodeRows = 48 * 148;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -238,14 +238,17 @@ attn_status_t launch_books(void (*kern)(P...), cudaStream_t st, A... args) {
     });
 }
 
+// Blocks of a copy kernel: a warp per span, up to four waves, so that a block that
+// finds padding or short pages makes way for another.
+int row_blocks(size_t spans) { return grid_for(spans, pg::kCopyThreads / 32, sm_count() * 32); }
+
 // At most `most` pages move.
 attn_status_t launch_moves(const pg::Books& k, void* Kp, void* Vp, int wk, int wv, int most, cudaStream_t st) {
-    const size_t spans = pg::spans_of(static_cast<size_t>(wk) << k.g.page_log2) +
-                         pg::spans_of(static_cast<size_t>(wv) << k.g.page_log2);
-    const int grid = grid_for(spans * most * k.g.Hkv, pg::kCopyThreads / 32, sm_count() * 8);
+    const pg::RowPlan plan = pg::RowPlan::of(wk, wv, 1 << k.g.page_log2, k.g.Hkv);
+    const int grid = row_blocks(static_cast<size_t>(plan.spans.d) * most * k.g.Hkv);
     return traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
         return launch_dependent(pg::move_rows, dim3(grid), pg::kCopyThreads, st, k.g, static_cast<uint4*>(Kp),
-                                static_cast<uint4*>(Vp), k.control, k.moves, wk, wv)
+                                static_cast<uint4*>(Vp), k.control, k.moves, plan)
                    ? launched()
                    : ATTN_ERR_CUDA;
     });
@@ -326,7 +329,8 @@ attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, voi
     pg::Geometry g;
     attn_status_t s = check_cache(B, Hkv, d, dv, num_pages, page, max_pages, dtype, &g);
     if (s != ATTN_OK) return s;
-    if (n < 1 || static_cast<double>(B) * Hkv * n >= 2147483648.0) return ATTN_ERR_SHAPE;
+    // The copy kernel numbers spans of at least one row, of K and of V, below 2^31.
+    if (n < 1 || 2.0 * B * Hkv * n >= 2147483648.0) return ATTN_ERR_SHAPE;
     if (!K || !V || !K_pages || !V_pages || !table || !lens || !ref || !table_out || !lens_out || !ref_out || !info)
         return ATTN_ERR_NULL;
     if (!aligned16(K) || !aligned16(V) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned4(table) ||
@@ -350,12 +354,12 @@ attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, voi
     s = launch_books(pg::append_books, st, k, new_len, n);
     if (s != ATTN_OK) return s;
     const int wk = d * es / 16, wv = dv * es / 16;
-    const size_t spans = pg::spans_of(static_cast<size_t>(n) * wk) + pg::spans_of(static_cast<size_t>(n) * wv);
-    const int grid = grid_for(spans * B * Hkv, pg::kCopyThreads / 32, sm_count() * 8);
+    const pg::RowPlan plan = pg::RowPlan::of(wk, wv, n, Hkv);
+    const int grid = row_blocks(static_cast<size_t>(plan.spans.d) * B * Hkv);
     s = traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
         return launch_dependent(pg::append_rows, dim3(grid), pg::kCopyThreads, st, g, static_cast<const uint4*>(K),
                                 static_cast<const uint4*>(V), static_cast<uint4*>(K_pages),
-                                static_cast<uint4*>(V_pages), table_out, k.control, k.start, k.after, n, wk, wv)
+                                static_cast<uint4*>(V_pages), table_out, k.control, k.start, k.after, n, plan)
                    ? launched()
                    : ATTN_ERR_CUDA;
     });
