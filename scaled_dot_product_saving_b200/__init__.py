@@ -388,43 +388,39 @@ def _opt(t, name, shape, dtype, dev):
 
 
 def _pools(k_pages, v_pages, table):
-    """Device index, dtype, library code, (P, Hkv, page, d, dv, B, M), pools' addresses."""
-    _require(k_pages, v_pages)
+    """Device index, dtype, (P, Hkv, page, d, dv, B, M), pools' addresses."""
     try:
+        dev, dt = k_pages.get_device(), k_pages.dtype
         P, Hkv, page, d = k_pages.shape
         dv = v_pages.shape[3]
         B, M = table.shape
     except (ValueError, IndexError, AttributeError):
         raise ValueError("a cache is [P, Hkv, page, d] and [P, Hkv, page, dv] pages and an int32 "
                          "[B, max_pages] table") from None
-    dev, dt = k_pages.get_device(), k_pages.dtype
-    return (dev, dt, dtype_code(dt), (P, Hkv, page, d, dv, B, M), k_pages.data_ptr(),
-            _arg(v_pages, "v_pages", (P, Hkv, page, dv), dt, dev))
+    if dev < 0 or not k_pages.is_contiguous():
+        raise ValueError("tensors must be contiguous and live on a CUDA device")
+    return dev, dt, P, Hkv, page, d, dv, B, M, k_pages.data_ptr(), _arg(v_pages, "v_pages", (P, Hkv, page, dv), dt, dev)
 
 
 class _On:
     """The device of a call's tensors and the stream it runs on made current,
-    so that what the binding allocates belongs to that stream. Gives the
-    stream's handle."""
+    so that what the binding allocates belongs to that stream."""
 
     def __init__(self, dev, stream):
-        self._held = []
-        if stream is not None:
-            if stream.device_index != dev:
-                raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{dev}")
-            self._held.append(torch.cuda.stream(stream))       # its device, too
-        elif torch.cuda.current_device() != dev:
-            self._held.append(torch.cuda.device(dev))
-        self._dev = dev
+        if stream is not None and stream.device_index != dev:
+            raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{dev}")
+        self._held = [torch.cuda.device(dev)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
-    def __enter__(self) -> int:
+    def __enter__(self):
         for c in self._held:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self._dev)
 
     def __exit__(self, *e):
         for c in reversed(self._held):
             c.__exit__(*e)
+
+
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _new(t, shape, dtype, dev):
@@ -457,22 +453,26 @@ def attn_decode(q, k_pages, v_pages, table, lens, causal=True, scale=None, q_len
     query i of c is token lens[b] - c + i and sees the tokens up to itself.
     q_len (optional int32 [B]): queries of each sequence; rows past it are left
     as they were (undefined in an `out` that this call allocates)."""
-    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
+    dev, dt, P, Hkv, page, d, dvw, B, M, kp, vp = _pools(k_pages, v_pages, table)
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return attn_decode(q, k_pages, v_pages, table, lens, causal, scale, q_len, out, lse, workspace)
+    code = dtype_code(dt)
     if q.dim() != 4:
         raise ValueError("q must be a [B, H, n, d] tensor")
     H, n = q.shape[1], q.shape[2]
     scale = 1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale)
-    with _On(dev, stream) as st:
-        out = _new(out, (B, H, n, dvw), dt, dev)
-        lse = _new(lse, (B, H, n), _f32, dev)
-        if workspace is None:
-            workspace = _scratch(None, attn_decode_workspace_size(B, H, Hkv, n, d, dvw, code), dev)
-        ws = _scratch(workspace, 0, dev)
-        status = lib.attn_decode(
-            _arg(q, "q", (B, H, n, d), dt, dev), kp, vp, _arg(table, "table", (B, M), _i32, dev),
-            _arg(lens, "lens", (B,), _i32, dev), _opt(q_len, "q_len", (B,), _i32, dev),
-            _arg(out, "out", (B, H, n, dvw), dt, dev), _arg(lse, "lse", (B, H, n), _f32, dev),
-            ws.data_ptr(), ws.nbytes, B, H, Hkv, n, d, dvw, P, page, M, code, 1 if causal else 0, scale, st)
+    out = _new(out, (B, H, n, dvw), dt, dev)
+    lse = _new(lse, (B, H, n), _f32, dev)
+    if workspace is None:
+        workspace = _scratch(None, attn_decode_workspace_size(B, H, Hkv, n, d, dvw, code), dev)
+    ws = _scratch(workspace, 0, dev)
+    status = lib.attn_decode(
+        _arg(q, "q", (B, H, n, d), dt, dev), kp, vp, _arg(table, "table", (B, M), _i32, dev),
+        _arg(lens, "lens", (B,), _i32, dev), _opt(q_len, "q_len", (B,), _i32, dev),
+        _arg(out, "out", (B, H, n, dvw), dt, dev), _arg(lse, "lse", (B, H, n), _f32, dev),
+        ws.data_ptr(), ws.nbytes, B, H, Hkv, n, d, dvw, P, page, M, code, 1 if causal else 0, scale,
+        _raw_stream(dev))
     if status != ATTN_OK:
         raise AttnError(status, "attn_decode")
     return out, lse
@@ -484,23 +484,27 @@ def attn_cache_append(k, v, k_pages, v_pages, table, lens, ref, new_len=None, ta
     (table, lens, ref, info) after it. Pass table_out=table and so on to work
     in place. new_len (optional int32 [B]): valid rows of each sequence.
     info [3]: status (0: done), free pages, pages taken."""
-    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
+    dev, dt, P, Hkv, page, d, dvw, B, M, kp, vp = _pools(k_pages, v_pages, table)
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return attn_cache_append(k, v, k_pages, v_pages, table, lens, ref, new_len, table_out, lens_out, ref_out,
+                                     info, workspace)
+    code = dtype_code(dt)
     if k.dim() != 4:
         raise ValueError("k must be a [B, Hkv, n, d] tensor")
     n = k.shape[2]
-    with _On(dev, stream) as st:
-        table_out, lens_out = _new(table_out, (B, M), _i32, dev), _new(lens_out, (B,), _i32, dev)
-        ref_out, info = _new(ref_out, (P,), _i32, dev), _new(info, (3,), _i32, dev)
-        if workspace is None:
-            workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
-        ws = _scratch(workspace, 0, dev)
-        status = lib.attn_cache_append(
-            _arg(k, "k", (B, Hkv, n, d), dt, dev), _arg(v, "v", (B, Hkv, n, dvw), dt, dev), kp, vp,
-            _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
-            _arg(ref, "ref", (P,), _i32, dev), _opt(new_len, "new_len", (B,), _i32, dev),
-            _arg(table_out, "table_out", (B, M), _i32, dev), _arg(lens_out, "lens_out", (B,), _i32, dev),
-            _arg(ref_out, "ref_out", (P,), _i32, dev), _arg(info, "info", (3,), _i32, dev),
-            ws.data_ptr(), ws.nbytes, B, Hkv, n, d, dvw, P, page, M, code, st)
+    table_out, lens_out = _new(table_out, (B, M), _i32, dev), _new(lens_out, (B,), _i32, dev)
+    ref_out, info = _new(ref_out, (P,), _i32, dev), _new(info, (3,), _i32, dev)
+    if workspace is None:
+        workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
+    ws = _scratch(workspace, 0, dev)
+    status = lib.attn_cache_append(
+        _arg(k, "k", (B, Hkv, n, d), dt, dev), _arg(v, "v", (B, Hkv, n, dvw), dt, dev), kp, vp,
+        _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
+        _arg(ref, "ref", (P,), _i32, dev), _opt(new_len, "new_len", (B,), _i32, dev),
+        _arg(table_out, "table_out", (B, M), _i32, dev), _arg(lens_out, "lens_out", (B,), _i32, dev),
+        _arg(ref_out, "ref_out", (P,), _i32, dev), _arg(info, "info", (3,), _i32, dev),
+        ws.data_ptr(), ws.nbytes, B, Hkv, n, d, dvw, P, page, M, code, _raw_stream(dev))
     if status != ATTN_OK:
         raise AttnError(status, "attn_cache_append")
     return table_out, lens_out, ref_out, info
@@ -512,20 +516,24 @@ def attn_cache_fork(k_pages, v_pages, table, lens, ref, src, keep=None, table_ou
     src[b] (int32 [B]; outside [0, B): b ends); returns (table, lens, ref,
     info) after it. Forks, beam reordering, shared prefixes, roll-back and
     freeing. info [3]: status (0: done), free pages, pages copied."""
-    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
-    with _On(dev, stream) as st:
-        table_out, lens_out = _new(table_out, (B, M), _i32, dev), _new(lens_out, (B,), _i32, dev)
-        ref_out, info = _new(ref_out, (P,), _i32, dev), _new(info, (3,), _i32, dev)
-        if workspace is None:
-            workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
-        ws = _scratch(workspace, 0, dev)
-        status = lib.attn_cache_fork(
-            kp, vp, _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
-            _arg(ref, "ref", (P,), _i32, dev), _arg(src, "src", (B,), _i32, dev),
-            _opt(keep, "keep", (B,), _i32, dev), _arg(table_out, "table_out", (B, M), _i32, dev),
-            _arg(lens_out, "lens_out", (B,), _i32, dev), _arg(ref_out, "ref_out", (P,), _i32, dev),
-            _arg(info, "info", (3,), _i32, dev), ws.data_ptr(), ws.nbytes, B, Hkv, d, dvw, P, page, M,
-            code, st)
+    dev, dt, P, Hkv, page, d, dvw, B, M, kp, vp = _pools(k_pages, v_pages, table)
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return attn_cache_fork(k_pages, v_pages, table, lens, ref, src, keep, table_out, lens_out, ref_out, info,
+                                   workspace)
+    code = dtype_code(dt)
+    table_out, lens_out = _new(table_out, (B, M), _i32, dev), _new(lens_out, (B,), _i32, dev)
+    ref_out, info = _new(ref_out, (P,), _i32, dev), _new(info, (3,), _i32, dev)
+    if workspace is None:
+        workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
+    ws = _scratch(workspace, 0, dev)
+    status = lib.attn_cache_fork(
+        kp, vp, _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
+        _arg(ref, "ref", (P,), _i32, dev), _arg(src, "src", (B,), _i32, dev),
+        _opt(keep, "keep", (B,), _i32, dev), _arg(table_out, "table_out", (B, M), _i32, dev),
+        _arg(lens_out, "lens_out", (B,), _i32, dev), _arg(ref_out, "ref_out", (P,), _i32, dev),
+        _arg(info, "info", (3,), _i32, dev), ws.data_ptr(), ws.nbytes, B, Hkv, d, dvw, P, page, M,
+        code, _raw_stream(dev))
     if status != ATTN_OK:
         raise AttnError(status, "attn_cache_fork")
     return table_out, lens_out, ref_out, info
@@ -536,19 +544,22 @@ def attn_cache_compact(k_pages, v_pages, table, lens, ref, table_out=None, ref_o
     """The live pages to the front of the pools; returns (table, ref, remap,
     info) after it. remap [P]: the new number of each page, -1 if free.
     info [3]: 0, free pages, pages moved."""
-    dev, dt, code, (P, Hkv, page, d, dvw, B, M), kp, vp = _pools(k_pages, v_pages, table)
-    with _On(dev, stream) as st:
-        table_out, ref_out = _new(table_out, (B, M), _i32, dev), _new(ref_out, (P,), _i32, dev)
-        remap, info = _new(remap, (P,), _i32, dev), _new(info, (3,), _i32, dev)
-        if workspace is None:
-            workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
-        ws = _scratch(workspace, 0, dev)
-        status = lib.attn_cache_compact(
-            kp, vp, _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
-            _arg(ref, "ref", (P,), _i32, dev), _arg(table_out, "table_out", (B, M), _i32, dev),
-            _arg(ref_out, "ref_out", (P,), _i32, dev), _arg(remap, "remap", (P,), _i32, dev),
-            _arg(info, "info", (3,), _i32, dev), ws.data_ptr(), ws.nbytes, B, Hkv, d, dvw, P, page, M,
-            code, st)
+    dev, dt, P, Hkv, page, d, dvw, B, M, kp, vp = _pools(k_pages, v_pages, table)
+    if stream is not None or _device() != dev:
+        with _On(dev, stream):
+            return attn_cache_compact(k_pages, v_pages, table, lens, ref, table_out, ref_out, remap, info, workspace)
+    code = dtype_code(dt)
+    table_out, ref_out = _new(table_out, (B, M), _i32, dev), _new(ref_out, (P,), _i32, dev)
+    remap, info = _new(remap, (P,), _i32, dev), _new(info, (3,), _i32, dev)
+    if workspace is None:
+        workspace = _scratch(None, attn_cache_workspace_size(B, M, P), dev)
+    ws = _scratch(workspace, 0, dev)
+    status = lib.attn_cache_compact(
+        kp, vp, _arg(table, "table", (B, M), _i32, dev), _arg(lens, "lens", (B,), _i32, dev),
+        _arg(ref, "ref", (P,), _i32, dev), _arg(table_out, "table_out", (B, M), _i32, dev),
+        _arg(ref_out, "ref_out", (P,), _i32, dev), _arg(remap, "remap", (P,), _i32, dev),
+        _arg(info, "info", (3,), _i32, dev), ws.data_ptr(), ws.nbytes, B, Hkv, d, dvw, P, page, M,
+        code, _raw_stream(dev))
     if status != ATTN_OK:
         raise AttnError(status, "attn_cache_compact")
     return table_out, ref_out, remap, info

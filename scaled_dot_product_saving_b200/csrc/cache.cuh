@@ -7,8 +7,7 @@
 // cluster of kBookCtas CTAs: their phases depend on one another through counts
 // over all pages, and a cluster's hardware barrier separates them without a
 // launch per phase. They work from device memory only, never through the
-// host, and leave the list of rows to move in the workspace for the copy
-// kernel launched after them.
+// host, and leave the list of rows to move in the workspace.
 //
 // What bounds the books is latency: a phase is two or three dependent reads of
 // L2 and a barrier, about 2 us, whatever the sizes up to some ten thousand
@@ -122,15 +121,220 @@ __device__ __forceinline__ void table_blocks(const Geometry& g, F&& f) {
     }
 }
 
+// -------------------------------------------------------------- copying rows
+// A warp takes a span at a time: up to kSpan 16-byte units (four a lane in
+// flight) of consecutive rows of K, or of V. Spans are whole rows, so that where
+// a lane's units lie in a row is the same in every span, and the loops divide by
+// multiplication. Copies of up to kHereSpans spans are made by the cluster that
+// keeps the books; larger ones by a kernel of their own over the whole GPU, which
+// starts while the books are still being written and reads what it needs of
+// them from L2, after its wait.
+constexpr int kCopyThreads = 256, kUnits = 4, kSpan = 32 * kUnits;
+constexpr unsigned kHereSpans = 512;
+
+// n / d for 0 <= n < 2^31.
+struct Divisor {
+    unsigned d, mul, shift;
+    static Divisor of(unsigned d) {
+        unsigned l = 0;
+        while (l < 31 && (1u << l) < d) ++l;
+        return Divisor{d, unsigned(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+    }
+    __device__ __forceinline__ unsigned divide(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+// What is copied. Widths in 16-byte units. A part is a run of rows that spans do
+// not cross: one head of a page to move; of new rows one head of a sequence, or,
+// when that is less than four spans (few tokens a sequence), all of them.
+struct Rows {
+    const uint4* K;      // append: the new rows [B, Hkv, n, w]
+    const uint4* V;
+    uint4* Kp;
+    uint4* Vp;
+    int n;
+    int wk, wv, k_rows, v_rows;              // widths, rows of a span
+    unsigned k_spans;                        // of a part's K; the rest are of its V
+    Divisor spans, by_n, by_heads;           // spans of a part
+    bool flat;                               // append: one part
+    bool here;                               // by the books' own cluster
+
+    static Rows of(void* Kp, void* Vp, int wk, int wv, long long rows, int heads, int n, bool flat) {
+        Rows r{};
+        r.Kp = static_cast<uint4*>(Kp);
+        r.Vp = static_cast<uint4*>(Vp);
+        r.n = n;
+        r.wk = wk;
+        r.wv = wv;
+        r.k_rows = kSpan / wk;
+        r.v_rows = kSpan / wv;
+        r.k_spans = unsigned((rows + r.k_rows - 1) / r.k_rows);
+        r.spans = Divisor::of(r.k_spans + unsigned((rows + r.v_rows - 1) / r.v_rows));
+        r.by_n = Divisor::of(n);
+        r.by_heads = Divisor::of(heads);
+        r.flat = flat;
+        return r;
+    }
+    static Rows of_new(void* Kp, void* Vp, int wk, int wv, int B, int heads, int n) {
+        const bool flat = n < 4 * (kSpan / wk);
+        return of(Kp, Vp, wk, wv, flat ? 1ll * B * heads * n : n, heads, n, flat);
+    }
+};
+
+// Span x of the new rows, all of them one part, to their pages. `wait` is called
+// once the rows are on their way, if `early`, and says whether to go on.
+template <typename F>
+__device__ __forceinline__ bool append_span_flat(const Books& k, const Rows& r, unsigned x, bool early, F&& wait) {
+    const Geometry& g = k.g;
+    const int lane = threadIdx.x & 31, page = 1 << g.page_log2;
+    const bool is_v = x >= r.k_spans;
+    const unsigned w = is_v ? r.wv : r.wk, span_rows = is_v ? r.v_rows : r.k_rows;
+    const unsigned row0 = (is_v ? x - r.k_spans : x) * span_rows;      // of all new rows
+    const unsigned rows = min(span_rows, unsigned(g.B) * g.Hkv * r.n - row0);
+    const uint4* from = (is_v ? r.V : r.K) + size_t(row0) * w + lane;
+    uint4* pool = is_v ? r.Vp : r.Kp;
+    uint4 v[kUnits];
+    unsigned c[kUnits];
+    int b[kUnits], h[kUnits], i[kUnits], t[kUnits];
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+        const unsigned u = lane + 32 * e, row = u / w;
+        c[e] = u - row * w;
+        b[e] = -1;
+        if (row >= rows) continue;
+        const unsigned bh = r.by_n.divide(row0 + row);
+        i[e] = int(row0 + row - bh * r.n);
+        b[e] = int(r.by_heads.divide(bh));
+        h[e] = int(bh - b[e] * r.by_heads.d);
+        v[e] = __ldcs(from + 32 * e);
+    }
+    if (early && !wait()) return false;
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+        if (b[e] < 0) continue;
+        t[e] = __ldcg(k.start + b[e]) + i[e];
+        if (t[e] >= __ldcg(k.after + b[e])) b[e] = -1;
+        else i[e] = __ldcg(k.table_out + size_t(b[e]) * g.M + (t[e] >> g.page_log2));
+    }
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e)
+        if (b[e] >= 0 && page_ok(i[e], g.P))
+            pool[((size_t(i[e]) * g.Hkv + h[e]) * page + (t[e] & (page - 1))) * w + c[e]] = v[e];
+    return true;
+}
+
+// Where a lane's units lie in a span of rows of w units.
+struct Lanes {
+    int row[kUnits], col[kUnits];
+    __device__ __forceinline__ Lanes(int w, int rows) {
+#pragma unroll
+        for (int e = 0; e < kUnits; ++e) {
+            const int u = (threadIdx.x & 31) + 32 * e;
+            row[e] = u / w;
+            col[e] = u - row[e] * w;
+            if (row[e] >= rows) row[e] = 0x3fffffff;       // past the span
+        }
+    }
+};
+
+// Span x of the new rows, a part for each head of a sequence.
+__device__ __forceinline__ void append_span(const Books& k, const Rows& r, unsigned x, const Lanes& in_k,
+                                            const Lanes& in_v) {
+    const Geometry& g = k.g;
+    const int page = 1 << g.page_log2;
+    const unsigned bh = r.spans.divide(x), b = r.by_heads.divide(bh), h = bh - b * r.by_heads.d;
+    unsigned span = x - bh * r.spans.d;
+    const bool is_v = span >= r.k_spans;
+    if (is_v) span -= r.k_spans;
+    const int w = is_v ? r.wv : r.wk, i0 = int(span) * (is_v ? r.v_rows : r.k_rows);
+    // Rows that turn out to be padding are not worth reading.
+    const int t0 = __ldcg(k.start + b) + i0, left = __ldcg(k.after + b) - t0;
+    if (left <= 0) return;
+    const uint4* from = (is_v ? r.V : r.K) + (size_t(bh) * r.n + i0) * w + (threadIdx.x & 31);
+    uint4* pool = (is_v ? r.Vp : r.Kp);
+    const int* row = k.table_out + size_t(b) * g.M;
+    uint4 v[kUnits];
+    int p[kUnits];
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+        const int i = is_v ? in_v.row[e] : in_k.row[e];
+        if (i >= left) continue;
+        v[e] = __ldcs(from + 32 * e);
+        p[e] = __ldcg(row + ((t0 + i) >> g.page_log2));
+    }
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+        const int i = is_v ? in_v.row[e] : in_k.row[e], c = is_v ? in_v.col[e] : in_k.col[e];
+        if (i < left && page_ok(p[e], g.P))
+            pool[((size_t(p[e]) * g.Hkv + h) * page + ((t0 + i) & (page - 1))) * w + c] = v[e];
+    }
+}
+
+// Span x of the moves: rows [0, rows) of every head of the listed pages.
+__device__ __forceinline__ void move_span(const Books& k, const Rows& r, unsigned long long x) {
+    const Geometry& g = k.g;
+    const int lane = threadIdx.x & 31;
+    const unsigned qh = (x >> 31) == 0 ? r.spans.divide(unsigned(x)) : unsigned(x / r.spans.d);
+    const unsigned q = r.by_heads.divide(qh), h = qh - q * r.by_heads.d;
+    unsigned span = unsigned(x - (unsigned long long)qh * r.spans.d);
+    const bool is_v = span >= r.k_spans;
+    if (is_v) span -= r.k_spans;
+    const int w = is_v ? r.wv : r.wk, rows = is_v ? r.v_rows : r.k_rows;
+    const int4 m = __ldcg(reinterpret_cast<const int4*>(k.moves) + q);
+    const int units = min(rows, m.z - int(span) * rows) * w, u0 = int(span) * rows * w + lane;
+    uint4* pool = is_v ? r.Vp : r.Kp;
+    const uint4* from = pool + ((size_t(m.x) * g.Hkv + h) << g.page_log2) * w + u0;
+    uint4* to = pool + ((size_t(m.y) * g.Hkv + h) << g.page_log2) * w + u0;
+    uint4 v[kUnits];
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e)
+        if (lane + 32 * e < units) v[e] = __ldcs(from + 32 * e);
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e)
+        if (lane + 32 * e < units) __stcs(to + 32 * e, v[e]);
+}
+
+__global__ void __launch_bounds__(kCopyThreads) append_rows(Books k, Rows r) {
+    const unsigned stride = gridDim.x * (kCopyThreads / 32), first = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+    auto wait = [&] {
+        grid_dependency_wait();
+        return __ldcg(k.control + kCtlMoves) != 0;
+    };
+    if (r.flat) {
+        // The first rows are on the way before the books are read.
+        for (unsigned x = first; x < r.spans.d; x += stride)
+            if (!append_span_flat(k, r, x, x == first, wait)) return;
+    } else {
+        if (!wait()) return;
+        const Lanes in_k(r.wk, r.k_rows), in_v(r.wv, r.v_rows);
+        const unsigned items = r.spans.d * unsigned(k.g.B) * unsigned(k.g.Hkv);
+        for (unsigned x = first; x < items; x += stride) append_span(k, r, x, in_k, in_v);
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) move_rows(Books k, Rows r) {
+    grid_dependency_wait();
+    const unsigned long long items = (unsigned long long)__ldcg(k.control + kCtlMoves) * k.g.Hkv * r.spans.d;
+    const unsigned stride = gridDim.x * (kCopyThreads / 32);
+    for (unsigned long long x = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items; x += stride)
+        move_span(k, r, x);
+}
+
+// The moves by the books' cluster, after its last writes.
+__device__ __forceinline__ void move_here(const Books& k, const Rows& r) {
+    cluster_sync();
+    const unsigned items = unsigned(__ldcg(k.control + kCtlMoves)) * k.g.Hkv * r.spans.d;
+    for (unsigned x = cluster_rank() * kBookWarps + (threadIdx.x >> 5); x < items; x += kAllWarps) move_span(k, r, x);
+}
+
 // ------------------------------------------------------------------- append
-__global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const int* new_len, int n) {
+__global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const int* new_len, Rows r) {
     grid_launch_dependents();                       // the copy kernel may set up meanwhile
     __shared__ long long scratch[33];
     __shared__ int full_s, shared_s;
     const Geometry& g = k.g;
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = int(cluster_rank());
-    const int page_mask = (1 << g.page_log2) - 1, room = g.M << g.page_log2;
+    const int page_mask = (1 << g.page_log2) - 1, room = g.M << g.page_log2, n = r.n;
     const bool same_ref = k.ref_out == k.ref, same_table = k.table_out == k.table;
     if (tid == 0) full_s = shared_s = 0;
 
@@ -243,134 +447,10 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const i
             else if (k.lens_out != k.lens) k.lens_out[b] = k.lens[b];
         }
     }
-}
-
-// The copy kernels start while the books are still being written: what they
-// read of them they read from L2, after the wait.
-//
-// A warp takes a span at a time: up to kSpan 16-byte units (four a lane in
-// flight) of the rows of K, or of V, of one head of a sequence or page. Spans are
-// whole rows, so that where a lane's units lie in a row is the same in every
-// span, and the loop divides by multiplication: with 64-bit divisions the rows
-// of a large append were bound by instructions (37 us against 42 for 134 MB).
-constexpr int kCopyThreads = 256, kUnits = 4, kSpan = 32 * kUnits;
-
-// n / d for 0 <= n < 2^31.
-struct Divisor {
-    unsigned d, mul, shift;
-    static Divisor of(unsigned d) {
-        unsigned l = 0;
-        while (l < 31 && (1u << l) < d) ++l;
-        return Divisor{d, unsigned(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
-    }
-    __device__ __forceinline__ unsigned divide(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
-};
-
-// Widths in 16-byte units, rows a span, and spans of a head's K and of its K and V.
-struct RowPlan {
-    int wk, wv, k_rows, v_rows;
-    unsigned k_spans;
-    Divisor spans, heads;
-    static RowPlan of(int wk, int wv, long long rows, int heads) {
-        RowPlan p{wk, wv, kSpan / wk, kSpan / wv, 0, {}, {}};
-        p.k_spans = unsigned((rows + p.k_rows - 1) / p.k_rows);
-        p.spans = Divisor::of(p.k_spans + unsigned((rows + p.v_rows - 1) / p.v_rows));
-        p.heads = Divisor::of(heads);
-        return p;
-    }
-};
-
-// New rows K [B, Hkv, n, wk], V [B, Hkv, n, wv] into their pages.
-__global__ void __launch_bounds__(kCopyThreads)
-append_rows(Geometry g, const uint4* __restrict__ K, const uint4* __restrict__ V, uint4* __restrict__ Kp,
-            uint4* __restrict__ Vp, const int* table, const int* control, const int* start, const int* after,
-            int n, RowPlan plan) {
-    const int lane = threadIdx.x & 31, page = 1 << g.page_log2;
-    const unsigned items = plan.spans.d * unsigned(g.B) * unsigned(g.Hkv), stride = gridDim.x * (kCopyThreads / 32);
-    // Of a small call (one token a sequence) the rows are on the way before the
-    // books are read; of a large one, rows that may be padding are not.
-    const bool early = items <= min(stride, 2048u);
-    if (!early) {
-        grid_dependency_wait();
-        if (!__ldcg(control + kCtlMoves)) return;
-    }
-    // This lane's units of a span: row and column, in K's rows and in V's.
-    int ki[kUnits], kc[kUnits], vi[kUnits], vc[kUnits];
-#pragma unroll
-    for (int e = 0; e < kUnits; ++e) {
-        const int u = lane + 32 * e;
-        ki[e] = u / plan.wk;
-        kc[e] = u - ki[e] * plan.wk;
-        if (ki[e] >= plan.k_rows) ki[e] = 0x3fffffff;
-        vi[e] = u / plan.wv;
-        vc[e] = u - vi[e] * plan.wv;
-        if (vi[e] >= plan.v_rows) vi[e] = 0x3fffffff;
-    }
-    for (unsigned x = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items; x += stride) {
-        const unsigned bh = plan.spans.divide(x), b = plan.heads.divide(bh), h = bh - b * plan.heads.d;
-        unsigned span = x - bh * plan.spans.d;
-        const bool is_v = span >= plan.k_spans;
-        if (is_v) span -= plan.k_spans;
-        const int w = is_v ? plan.wv : plan.wk;
-        const int i0 = int(span) * (is_v ? plan.v_rows : plan.k_rows);
-        const uint4* from = (is_v ? V : K) + (size_t(bh) * n + i0) * w + lane;
-        uint4* pool = is_v ? Vp : Kp;
-        int t0 = 0, left = n - i0;                   // new rows from i0 on
-        if (!early) {
-            t0 = __ldcg(start + b);
-            left = __ldcg(after + b) - t0 - i0;
-            if (left <= 0) continue;
-        }
-        uint4 v[kUnits];
-#pragma unroll
-        for (int e = 0; e < kUnits; ++e)
-            if ((is_v ? vi[e] : ki[e]) < left) v[e] = __ldcs(from + 32 * e);
-        if (early) {
-            grid_dependency_wait();
-            if (!__ldcg(control + kCtlMoves)) return;
-            t0 = __ldcg(start + b);
-            left = __ldcg(after + b) - t0 - i0;
-        }
-        t0 += i0;
-#pragma unroll
-        for (int e = 0; e < kUnits; ++e) {
-            const int i = is_v ? vi[e] : ki[e];
-            if (i >= left) continue;
-            const int t = t0 + i;
-            const int p = __ldcg(table + size_t(b) * g.M + (t >> g.page_log2));
-            if (page_ok(p, g.P))
-                pool[((size_t(p) * g.Hkv + h) * page + (t & (page - 1))) * w + (is_v ? vc[e] : kc[e])] = v[e];
-        }
-    }
-}
-
-// Rows [0, rows) of every head of the listed pages.
-__global__ void __launch_bounds__(kCopyThreads)
-move_rows(Geometry g, uint4* Kp, uint4* Vp, const int* control, const Move* moves, RowPlan plan) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    // At most P / 2 pages of Hkv heads move: below 2^30 items of few spans each.
-    const unsigned long long items = (unsigned long long)__ldcg(control + kCtlMoves) * g.Hkv * plan.spans.d;
-    const unsigned stride = gridDim.x * (kCopyThreads / 32);
-    for (unsigned long long x = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < items; x += stride) {
-        const unsigned qh = (x >> 31) == 0 ? plan.spans.divide(unsigned(x)) : unsigned(x / plan.spans.d);
-        const unsigned q = plan.heads.divide(qh), h = qh - q * plan.heads.d;
-        unsigned span = unsigned(x - (unsigned long long)qh * plan.spans.d);
-        const bool is_v = span >= plan.k_spans;
-        if (is_v) span -= plan.k_spans;
-        const int w = is_v ? plan.wv : plan.wk, rows = is_v ? plan.v_rows : plan.k_rows;
-        const int4 m = __ldcg(reinterpret_cast<const int4*>(moves) + q);
-        const int units = min(rows, m.z - int(span) * rows) * w, u0 = int(span) * rows * w + lane;
-        uint4* pool = is_v ? Vp : Kp;
-        const uint4* from = pool + ((size_t(m.x) * g.Hkv + h) << g.page_log2) * w + u0;
-        uint4* to = pool + ((size_t(m.y) * g.Hkv + h) << g.page_log2) * w + u0;
-        uint4 v[kUnits];
-#pragma unroll
-        for (int e = 0; e < kUnits; ++e)
-            if (lane + 32 * e < units) v[e] = __ldcs(from + 32 * e);
-#pragma unroll
-        for (int e = 0; e < kUnits; ++e)
-            if (lane + 32 * e < units) __stcs(to + 32 * e, v[e]);
+    if (r.here && ok) {
+        cluster_sync();
+        for (unsigned x = rank * kBookWarps + (tid >> 5); x < r.spans.d; x += kAllWarps)
+            append_span_flat(k, r, x, false, [] { return true; });
     }
 }
 
@@ -381,7 +461,7 @@ move_rows(Geometry g, uint4* Kp, uint4* Vp, const int* control, const Move* move
 // counts who holds p besides its takers as a last page. With base(p) = 0 one
 // taker keeps p (the one it belonged to, else the lowest: the least of `key`);
 // every other taker gets a copy in a fresh page.
-__global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int* src, const int* keep) {
+__global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int* src, const int* keep, Rows r) {
     grid_launch_dependents();                       // the copy kernel may set up meanwhile
     __shared__ long long scratch[33];
     const Geometry& g = k.g;
@@ -569,12 +649,13 @@ __global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int
     });
     if (k.lens_out == k.lens) cluster_sync();                    // every row has read its old length
     for (int b = b0; b < b1; ++b) k.lens_out[b] = one ? mine.L : k.after[b];
+    if (r.here) move_here(k, r);
 }
 
 // ------------------------------------------------------------------ compact
 // L live pages. The k-th live page at or past L moves to the k-th free page
 // before L: the fewest moves, no page both read and written.
-__global__ void __launch_bounds__(kBookThreads, 1) compact_books(Books k, int* remap) {
+__global__ void __launch_bounds__(kBookThreads, 1) compact_books(Books k, int* remap, Rows r) {
     grid_launch_dependents();                       // the copy kernel may set up meanwhile
     __shared__ long long scratch[33];
     const Geometry& g = k.g;
@@ -663,6 +744,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) compact_books(Books k, int* r
             if (j < end) k.table_out[row + j] = p[e];
         }
     });
+    if (r.here) move_here(k, r);
 }
 
 }  // namespace paged

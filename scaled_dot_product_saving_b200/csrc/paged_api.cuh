@@ -238,20 +238,24 @@ attn_status_t launch_books(void (*kern)(P...), cudaStream_t st, A... args) {
     });
 }
 
-// Blocks of a copy kernel: a warp per span, up to four waves, so that a block that
-// finds padding or short pages makes way for another.
-int row_blocks(size_t spans) { return grid_for(spans, pg::kCopyThreads / 32, sm_count() * 32); }
-
-// At most `most` pages move.
-attn_status_t launch_moves(const pg::Books& k, void* Kp, void* Vp, int wk, int wv, int most, cudaStream_t st) {
-    const pg::RowPlan plan = pg::RowPlan::of(wk, wv, 1 << k.g.page_log2, k.g.Hkv);
-    const int grid = row_blocks(static_cast<size_t>(plan.spans.d) * most * k.g.Hkv);
-    return traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
-        return launch_dependent(pg::move_rows, dim3(grid), pg::kCopyThreads, st, k.g, static_cast<uint4*>(Kp),
-                                static_cast<uint4*>(Vp), k.control, k.moves, plan)
-                   ? launched()
-                   : ATTN_ERR_CUDA;
+// The books, and the copies that they ask for: at most `spans` (see cache.cuh).
+template <typename Kern, typename A>
+attn_status_t books_and_rows(Kern kern, void (*copy)(pg::Books, pg::Rows), const pg::Books& k, pg::Rows r,
+                             unsigned long long spans, cudaStream_t st, A&& launch) {
+    r.here = spans <= pg::kHereSpans && (copy == pg::move_rows || r.flat);
+    attn_status_t s = launch(kern, r);
+    if (s != ATTN_OK || r.here) {
+        if (s == ATTN_OK) g_last_launches = 1;
+        return s;
+    }
+    // A warp per span, up to four waves, so that a block that finds padding or
+    // short pages makes way for another.
+    const int grid = grid_for(static_cast<size_t>(spans), pg::kCopyThreads / 32, sm_count() * 32);
+    s = traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
+        return launch_dependent(copy, dim3(grid), pg::kCopyThreads, st, k, r) ? launched() : ATTN_ERR_CUDA;
     });
+    if (s == ATTN_OK) g_last_launches = 2;
+    return s;
 }
 
 }  // namespace
@@ -351,20 +355,13 @@ attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, voi
 
     cudaStream_t st = as_stream(stream);
     const pg::Books k = books(g, table, lens, ref, table_out, lens_out, ref_out, info, workspace);
-    s = launch_books(pg::append_books, st, k, new_len, n);
-    if (s != ATTN_OK) return s;
-    const int wk = d * es / 16, wv = dv * es / 16;
-    const pg::RowPlan plan = pg::RowPlan::of(wk, wv, n, Hkv);
-    const int grid = row_blocks(static_cast<size_t>(plan.spans.d) * B * Hkv);
-    s = traced(ATTN_KERNEL_CACHE_ROWS, st, [&] {
-        return launch_dependent(pg::append_rows, dim3(grid), pg::kCopyThreads, st, g, static_cast<const uint4*>(K),
-                                static_cast<const uint4*>(V), static_cast<uint4*>(K_pages),
-                                static_cast<uint4*>(V_pages), table_out, k.control, k.start, k.after, n, plan)
-                   ? launched()
-                   : ATTN_ERR_CUDA;
+    pg::Rows r = pg::Rows::of_new(K_pages, V_pages, d * es / 16, dv * es / 16, B, Hkv, n);
+    r.K = static_cast<const uint4*>(K);
+    r.V = static_cast<const uint4*>(V);
+    const unsigned long long spans = r.flat ? r.spans.d : 1ull * r.spans.d * B * Hkv;
+    return books_and_rows(pg::append_books, pg::append_rows, k, r, spans, st, [&](auto kern, const pg::Rows& x) {
+        return launch_books(kern, st, k, new_len, x);
     });
-    if (s == ATTN_OK) g_last_launches = 2;
-    return s;
 }
 
 attn_status_t attn_cache_fork(void* K_pages, void* V_pages, const int* table, const int* lens, const int* ref,
@@ -394,12 +391,10 @@ attn_status_t attn_cache_fork(void* K_pages, void* V_pages, const int* table, co
 
     cudaStream_t st = as_stream(stream);
     const pg::Books k = books(g, table, lens, ref, table_out, lens_out, ref_out, info, workspace);
-    s = launch_books(pg::fork_books, st, k, src, keep);
     const int es = dtype == ATTN_F32 ? 4 : 2;
-    if (s == ATTN_OK)
-        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, B, st);
-    if (s == ATTN_OK) g_last_launches = 2;
-    return s;
+    const pg::Rows r = pg::Rows::of(K_pages, V_pages, d * es / 16, dv * es / 16, page, Hkv, 1, false);
+    return books_and_rows(pg::fork_books, pg::move_rows, k, r, 1ull * B * Hkv * r.spans.d, st,
+                          [&](auto kern, const pg::Rows& x) { return launch_books(kern, st, k, src, keep, x); });
 }
 
 attn_status_t attn_cache_compact(void* K_pages, void* V_pages, const int* table, const int* lens,
@@ -427,12 +422,10 @@ attn_status_t attn_cache_compact(void* K_pages, void* V_pages, const int* table,
 
     cudaStream_t st = as_stream(stream);
     const pg::Books k = books(g, table, lens, ref, table_out, nullptr, ref_out, info, workspace);
-    s = launch_books(pg::compact_books, st, k, remap);
     const int es = dtype == ATTN_F32 ? 4 : 2;
-    if (s == ATTN_OK)
-        s = launch_moves(k, K_pages, V_pages, d * es / 16, dv * es / 16, num_pages / 2 + 1, st);
-    if (s == ATTN_OK) g_last_launches = 2;
-    return s;
+    const pg::Rows r = pg::Rows::of(K_pages, V_pages, d * es / 16, dv * es / 16, page, Hkv, 1, false);
+    return books_and_rows(pg::compact_books, pg::move_rows, k, r, 1ull * (num_pages / 2) * Hkv * r.spans.d, st,
+                          [&](auto kern, const pg::Rows& x) { return launch_books(kern, st, k, remap, x); });
 }
 
 }  // extern "C"
