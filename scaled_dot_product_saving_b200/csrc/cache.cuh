@@ -62,17 +62,6 @@ struct Books {
     Move* moves;         // [max(B, P)]
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// All threads of the cluster meet, and see each other's earlier writes.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // The pages of this warp: a contiguous range, ranges in the order of
 // (CTA, warp), so that ranks follow page numbers.
 __device__ __forceinline__ void page_range(int P, int* lo, int* hi) {
@@ -470,33 +459,26 @@ __global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int
     const int page_mask = (1 << g.page_log2) - 1;
     const bool same_ref = k.ref_out == k.ref, same_table = k.table_out == k.table;
 
-    struct Seq {
-        int src, old_len, L;
-    };
-    auto seq = [&](int b) {
-        Seq q;
-        q.src = src[b];
-        q.old_len = clamp_len(k.lens[b], g);
-        const bool valid = q.src >= 0 && q.src < g.B;
-        q.L = valid ? clamp_len(k.lens[q.src], g) : 0;
-        if (valid && keep) q.L = min(max(keep[b], 0), q.L);
-        return q;
-    };
-
-    for (int p = rank * kBookThreads + tid; p < g.P; p += kAllThreads) {
-        k.base[p] = k.ref[p];
-        k.key[p] = kNone;
-    }
     // (First CTA) the last pages; a thread keeps its first sequence in registers.
     int b0 = 0, b1 = 0;
-    if (rank == 0) thread_share(g.B, &b0, &b1);
-    Seq mine{-1, 0, 0};
-    int tail = -1;
+    if (rank == 0) {
+        thread_share(g.B, &b0, &b1);
+    } else {
+#pragma unroll 4
+        for (int p = (rank - 1) * kBookThreads + tid; p < g.P; p += kAllThreads - kBookThreads) {
+            k.base[p] = k.ref[p];
+            k.key[p] = kNone;
+        }
+    }
+    int my_src = -1, my_L = 0, tail = -1;
     for (int b = b0; b < b1; ++b) {
-        mine = seq(b);
-        tail = (mine.L & page_mask) != 0 ? k.table[size_t(mine.src) * g.M + (mine.L >> g.page_log2)] : -1;
+        my_src = src[b];
+        const bool valid = my_src >= 0 && my_src < g.B;
+        my_L = valid ? clamp_len(k.lens[my_src], g) : 0;
+        if (valid && keep) my_L = min(max(keep[b], 0), my_L);
+        tail = (my_L & page_mask) != 0 ? k.table[size_t(my_src) * g.M + (my_L >> g.page_log2)] : -1;
         k.start[b] = tail;
-        k.after[b] = mine.L;
+        k.after[b] = my_L;
     }
     const bool one = b1 - b0 <= 1;
     cluster_sync();
@@ -504,12 +486,12 @@ __global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int
     // Uses given up and taken; pages that a sequence keeps in its own row
     // cancel. Rows that come from elsewhere are staged: they may be overwritten.
     table_blocks(g, [&](int b, int j0) {
-        const Seq q = seq(b);
-        const int had = pages_of(q.old_len, g.page_log2), full = q.L >> g.page_log2;
-        const bool home = q.src == b;
+        const int had = pages_of(clamp_len(k.lens[b], g), g.page_log2), full = __ldcg(k.after + b) >> g.page_log2;
+        const int s = src[b];
+        const bool home = s == b;
         if (j0 >= max(had, full)) return;
         const int* own = k.table + size_t(b) * g.M;
-        const int* from = k.table + size_t(full > 0 ? q.src : b) * g.M;
+        const int* from = k.table + size_t(full > 0 ? s : b) * g.M;
 #pragma unroll
         for (int j = j0 + lane; j < j0 + kRowBlock; j += 32) {
             if (j < had && !(home && j < full)) {
@@ -526,9 +508,9 @@ __global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int
     // A last page that can be followed, or -1; its takers in order.
     auto tail_of = [&](int b) {
         const int p = one ? tail : k.start[b];
-        return ((one ? mine.L : k.after[b]) & page_mask) != 0 && page_ok(p, g.P) ? p : -1;
+        return ((one ? my_L : k.after[b]) & page_mask) != 0 && page_ok(p, g.P) ? p : -1;
     };
-    auto order_of = [&](int b) { return (one ? mine.src : src[b]) == b ? b : b + g.B; };
+    auto order_of = [&](int b) { return (one ? my_src : src[b]) == b ? b : b + g.B; };
     for (int b = b0; b < b1; ++b) {
         const int p = tail_of(b);
         if (p >= 0) atomicMin(k.key + p, order_of(b));
@@ -559,7 +541,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int
     if (rank == 0) {
         int q = int(before & 0x7fffffff);
         for (int b = b0; b < b1; ++b) {
-            const int L = one ? mine.L : k.after[b];
+            const int L = one ? my_L : k.after[b];
             if ((L & page_mask) == 0) continue;
             const bool c = one ? ncopy != 0 : copies(b);
             const int entry = b * g.M + (L >> g.page_log2);
@@ -648,7 +630,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) fork_books(Books k, const int
         }
     });
     if (k.lens_out == k.lens) cluster_sync();                    // every row has read its old length
-    for (int b = b0; b < b1; ++b) k.lens_out[b] = one ? mine.L : k.after[b];
+    for (int b = b0; b < b1; ++b) k.lens_out[b] = one ? my_L : k.after[b];
     if (r.here) move_here(k, r);
 }
 

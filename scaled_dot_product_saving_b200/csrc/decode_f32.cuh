@@ -51,7 +51,7 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
 
     Walker w;
     if (warp == C::kWarps) w.start(a);                     // while the barriers are set up
-    if (!set_up(parts, ring, smem, C::kWarps)) return;
+    if (!set_up<false>(parts, ring, smem, C::kWarps)) return;
     if (warp == C::kWarps) {
         produce<C>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns);
         return;

@@ -59,11 +59,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 
 // Collective over the block. False (for all threads) if an earlier kernel's
 // timeout has not been read, in which case the call does nothing.
-template <int kStages, int kGroups>
+template <bool kTeamed, int kStages, int kGroups>
 __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups>& ring, const uint8_t* smem,
                                        int consumers) {
     if (threadIdx.x == 0) {
-        parts.head[blockIdx.x].b = -1;
+        if (!kTeamed) parts.head[blockIdx.x].b = -1;
         const bool misaligned = (smem_addr(smem) & 1023u) != 0;
         if (misaligned) record_device_error(kErrTimeout);
         ring.abort = misaligned || *reinterpret_cast<volatile unsigned int*>(&g_device_error) != 0;
@@ -80,16 +80,16 @@ __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups
     __syncthreads();
     const bool skip = ring.abort != 0;
     __syncthreads();                                // every thread has read the flag
-    grid_launch_dependents();                       // the join may set up meanwhile
+    if (!kTeamed) grid_launch_dependents();         // the join may set up meanwhile
     return !skip;
 }
 
 // The producer warp. A tile is 64 / box pages (box = min(page, 64) tokens, one
 // lane each); 32 table entries are held across the warp and the next 32 are on
 // the way. C: the kernel's configuration.
-template <typename C, typename T, typename RingT>
+template <typename C, typename T, typename RingT, typename W>
 __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMap* tmV, const DecodeArgs& a,
-                                        const T* Q, Walker& w, RingT& ring, uint8_t* smem,
+                                        const T* Q, W& w, RingT& ring, uint8_t* smem,
                                         unsigned long long budget_ns) {
     constexpr int kStages = C::kStages;
     const int lane = threadIdx.x & 31;

@@ -23,6 +23,8 @@
 // from HBM (a 32 KB tile every 1,450 cycles).
 #pragma once
 
+#include <type_traits>
+
 #include "decode_ring.cuh"
 
 namespace attn {
@@ -30,7 +32,8 @@ namespace paged {
 
 constexpr int kKeyWarps = 4;                       // warps that share a tile's keys
 
-template <int DK, int DV, int R>                   // padded widths, groups of 16 query rows
+// DK, DV: padded widths; R: groups of 16 query rows; kTeamed: a team an item.
+template <int DK, int DV, int R, bool kTeamed>
 struct DecodeCfg {
     static constexpr int kPanelCols = 64, kKPanels = DK / 64, kVPanels = DV / 64;
     static constexpr int kKBytes = kKPanels * kPanelBytes;
@@ -46,7 +49,10 @@ struct DecodeCfg {
     // 21.6 with three, 22.6 with four).
     static constexpr int kCtasPerSm = R == 2 ? 1 : DK == 64 && DV == 64 ? 3 : 2;
     static constexpr int kStages = (R == 2 ? 128 : kCtasPerSm == 3 ? 64 : kInStage ? 96 : 72) * 1024 / kStageBytes;
-    static constexpr int kSmemBytes = kStages * kStageBytes + (kInStage ? 0 : R * kScratchBytes);
+    // A team's CTA leaves its output here for the others: [16][DV].
+    static constexpr int kOffTeam = kStages * kStageBytes + (kInStage ? 0 : R * kScratchBytes);
+    static constexpr int kSmemBytes = kOffTeam + (kTeamed ? 16 * DV * 4 : 0);
+    static_assert(!kTeamed || R == 1, "a team has one group of rows");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -73,26 +79,39 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-template <int DK, int DV, int R>
-__global__ void __launch_bounds__(DecodeCfg<DK, DV, R>::kThreads, DecodeCfg<DK, DV, R>::kCtasPerSm)
+// An address of this CTA's shared memory in another CTA of the cluster.
+__device__ __forceinline__ uint32_t of_member(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_member(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int DK, int DV, int R, bool kTeamed>
+__global__ void __launch_bounds__(DecodeCfg<DK, DV, R, kTeamed>::kThreads, DecodeCfg<DK, DV, R, kTeamed>::kCtasPerSm)
 decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DecodeArgs a,
           const __nv_bfloat16* __restrict__ Q, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE,
           Parts parts, unsigned long long budget_ns) {
-    using C = DecodeCfg<DK, DV, R>;
+    using C = DecodeCfg<DK, DV, R, kTeamed>;
     constexpr int kTileRows = 16 * R, kStages = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Ring<kStages, R> ring;
     __shared__ float stat_m[R][kKeyWarps][16], stat_l[R][kKeyWarps][16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    Walker w;
-    if (warp == kKeyWarps * R) w.start(a);                // while the barriers are set up
-    if (!set_up(parts, ring, smem, kKeyWarps * R)) return;
-    if (warp == kKeyWarps * R) {
-        produce<C>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns);
-        return;
-    }
+    __shared__ float2 team_ml[kTeamed ? 16 : 1];          // maximum and sum of each row, for the team
 
+    std::conditional_t<kTeamed, Member, Walker> w;
+    if (kTeamed || warp == kKeyWarps * R) w.start(a);     // while the barriers are set up
+    if (kTeamed && threadIdx.x < 16) team_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    const bool going = set_up<kTeamed>(parts, ring, smem, kKeyWarps * R);
+    if (!kTeamed && !going) return;
+
+    auto consume = [&] {
     // ---------------------------------------------------------- key warps
     const int kg = warp % kKeyWarps, mt = warp / kKeyWarps;
     const int g = lane >> 2, t4 = lane & 3;
@@ -146,7 +165,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             L1 = fmaf(stat_l[mt][x][g + 8], ex2(stat_m[mt][x][g + 8] - Z1), L1);
         }
         warp_arrive(&ring.joint[mt][1]);
-        const bool all = (at.flags & (kStarts | kEnds)) == (kStarts | kEnds);
+        const bool all = !kTeamed && (at.flags & (kStarts | kEnds)) == (kStarts | kEnds);
         const int ra = mt * 16 + g, rb = ra + 8;
         const bool put0 = ra < at.rows && (!all || query_of(a, at, ra) < at.nq);
         const bool put1 = rb < at.rows && (!all || query_of(a, at, rb) < at.nq);
@@ -154,8 +173,12 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         const float inv1 = all ? (L1 > 0.f ? 1.f / L1 : L1 == 0.f ? 0.f : L1) : 1.f;
         const size_t slot = (2 * size_t(blockIdx.x) + (at.flags & kStarts ? 1 : 0)) * kTileRows;
         const size_t to0 = (all ? size_t(at.row) : slot) + ra, to1 = to0 + 8;
+        float* team_o = reinterpret_cast<float*>(smem + C::kOffTeam);
         if (kg == 0 && t4 == 0) {
-            if (all) {
+            if constexpr (kTeamed) {
+                team_ml[ra] = make_float2(M0, L0);
+                team_ml[rb] = make_float2(M1, L1);
+            } else if (all) {
                 if (put0) LSE[to0] = (M0 + log2f(L0)) * kLn2;
                 if (put1) LSE[to1] = (M1 + log2f(L1)) * kLn2;
             } else {
@@ -178,6 +201,11 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 y.y += o.y;
                 y.z += o.z;
                 y.w += o.w;
+            }
+            if constexpr (kTeamed) {
+                *reinterpret_cast<float2*>(team_o + ra * DV + c) = make_float2(y.x, y.y);
+                *reinterpret_cast<float2*>(team_o + rb * DV + c) = make_float2(y.z, y.w);
+                continue;
             }
             if (c >= a.dv) continue;
             if (all) {
@@ -358,6 +386,53 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             if (C::kInStage) fence_proxy_async_smem();    // before the TMA writes there again
         }
         warp_arrive(&ring.empty[s]);
+    }
+    };
+
+    if (warp == kKeyWarps * R) {
+        if (going) produce<C>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns);
+    } else if (going) {
+        consume();
+    }
+    if constexpr (kTeamed) {
+        // The team joined: every CTA takes an eighth of the columns of all rows
+        // from all of them. No CTA leaves before its memory has been read, on
+        // whatever way it got here.
+        __syncwarp();
+        cluster_sync();
+        const int rank = int(cluster_rank()), kCols = DV / kTeam / 2;                 // pairs of columns
+        const int r = threadIdx.x / kCols, c = (rank * kCols + threadIdx.x % kCols) * 2;
+        const int rows = a.rows - (w.p.item % a.row_tiles) * 16;
+        if (w.p.nq > 0 && r < min(16, rows)) {
+            const int first = (w.p.item % a.row_tiles) * 16;
+            const size_t row = row_base(a, w.p.b, w.p.item / a.row_tiles) + first + r;
+            const uint32_t ml = smem_addr(&team_ml[r]), o = smem_addr(smem + C::kOffTeam) + (r * DV + c) * 4;
+            float2 x[kTeam], y[kTeam];
+#pragma unroll
+            for (int k = 0; k < kTeam; ++k) {
+                x[k] = ld_member(of_member(ml, k));
+                y[k] = ld_member(of_member(o, k));
+            }
+            float M = -INFINITY, L = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < kTeam; ++k) M = fmaxf(M, x[k].x);
+            const float Z = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int k = 0; k < kTeam; ++k) {
+                if (x[k].x == -INFINITY) continue;        // no keys there: its output was never written
+                const float f = ex2(x[k].x - Z);
+                L = fmaf(x[k].y, f, L);
+                y0 = fmaf(y[k].x, f, y0);
+                y1 = fmaf(y[k].y, f, y1);
+            }
+            const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;                // NaN stays
+            if ((first + r) % a.n < w.p.nq) {
+                if (c < a.dv) *reinterpret_cast<uint32_t*>(O + row * a.dv + c) = pack_bf16x2(y0 * inv, y1 * inv);
+                if (c == 0) LSE[row] = (M + log2f(L)) * kLn2;
+            }
+        }
+        __syncwarp();
+        cluster_sync();
     }
 }
 

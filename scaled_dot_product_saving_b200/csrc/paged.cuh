@@ -61,6 +61,17 @@ __device__ __forceinline__ T block_exclusive(T v, T* scratch, T* total) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster meet, and see each other's earlier writes.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // ------------------------------------------------- the split of a decode call
 // A call's work is counted in units. An item (sequence, key head, tile of query
 // rows) costs one per key tile (kTileKeys keys) and kItemUnits for its start
@@ -187,6 +198,35 @@ struct Walker {
         const long long longer = r * (q + 1);
         return int(x < longer ? divide(x, q + 1) : r + divide(x - longer, q));
     }
+};
+
+// A small call (few items, short rows of the table) is split otherwise: a team,
+// one cluster of kTeam CTAs, takes an item and joins it through its own shared
+// memory, in one launch.
+constexpr int kTeam = 8;
+
+struct Member {
+    Piece p;
+    bool left;
+    __device__ void start(const DecodeArgs& a) {
+        const int items = a.g.Hkv * a.row_tiles, rank = int(cluster_rank());
+        const int item = blockIdx.x / kTeam;
+        p.b = item / items;
+        p.item = item - p.b * items;
+        p.nq = queries_of(a, p.b);
+        p.len = clamp_len(__ldg(a.lens + p.b), a.g);
+        p.tiles = tiles_of(p.len);
+        p.t0 = int((long long)p.tiles * rank / kTeam);
+        p.t1 = int((long long)p.tiles * (rank + 1) / kTeam);
+        left = p.nq > 0 && p.t0 < p.t1;
+    }
+    __device__ bool next(const DecodeArgs&, Piece* to) {
+        if (!left) return false;
+        *to = p;
+        left = false;
+        return true;
+    }
+    __device__ int owner(long long) const { return 0; }
 };
 
 // Pieces of cut items go through the workspace: CTA c writes its piece that

@@ -133,11 +133,12 @@ attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg
 }
 
 // The kernels that stream tiles with the TMA. C: the kernel's configuration; T:
-// the element type, whose columns the maps' 128-byte rows hold.
+// the element type, whose columns the maps' 128-byte rows hold. teams: 0, or one
+// team for each of so many items.
 template <typename C, typename T, typename Kern>
 attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg::DecodeArgs& a, const void* Q,
                             const void* Kp, const void* Vp, void* O, float* LSE, const pg::Parts& parts, int* grid,
-                            cudaStream_t st) {
+                            int teams, cudaStream_t st) {
     CUtensorMap mk, mv;
     const int page = 1 << a.g.page_log2, heads = a.g.P * a.g.Hkv, box = std::min(page, pg::kTileKeys);
     constexpr auto type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -146,10 +147,26 @@ attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg:
         return ATTN_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    *grid = std::min(ctas_per_sm * sm_count(), std::min(kDecodeCtas, kDecodeRows / a.tile_rows));
+    *grid = teams > 0 ? teams * pg::kTeam
+                      : std::min(ctas_per_sm * sm_count(), std::min(kDecodeCtas, kDecodeRows / a.tile_rows));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(*grid);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = pg::kTeam;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = teams > 0 ? 1 : 0;
     return traced(kernel_id, st, [&] {
-        kern<<<*grid, C::kThreads, C::kSmemBytes, st>>>(mk, mv, a, static_cast<const T*>(Q), static_cast<T*>(O), LSE,
-                                                        parts, kWaitBudgetNs);
+        if (cudaLaunchKernelEx(&cfg, kern, mk, mv, a, static_cast<const T*>(Q), static_cast<T*>(O), LSE, parts,
+                               kWaitBudgetNs) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return ATTN_ERR_CUDA;
+        }
         return launched();
     });
 }
@@ -157,11 +174,24 @@ attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg:
 template <int DK, int DV, int R>
 attn_status_t decode_tc(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                         const pg::Parts& parts, int* grid, cudaStream_t st) {
-    using C = pg::DecodeCfg<DK, DV, R>;
+    using C = pg::DecodeCfg<DK, DV, R, false>;
     a.tile_rows = 16 * R;
     a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
-    return decode_stream<C, __nv_bfloat16>(pg::decode_tc<DK, DV, R>, ATTN_KERNEL_DECODE_TENSOR, C::kCtasPerSm, a, Q,
-                                           Kp, Vp, O, LSE, parts, grid, st);
+    if constexpr (R == 1) {
+        // Teams where their CTAs are all resident at once and no sequence can be
+        // longer than 8 tiles for each of a team's CTAs: one launch instead of two.
+        const long long items = 1ll * a.g.B * a.g.Hkv * a.row_tiles;
+        if (items * pg::kTeam <= C::kCtasPerSm * sm_count() &&
+            (1ll * a.g.M << a.g.page_log2) <= 8 * pg::kTeam * pg::kTileKeys) {
+            const attn_status_t s = decode_stream<pg::DecodeCfg<DK, DV, R, true>, __nv_bfloat16>(
+                pg::decode_tc<DK, DV, R, true>, ATTN_KERNEL_DECODE_TENSOR, C::kCtasPerSm, a, Q, Kp, Vp, O, LSE, parts,
+                grid, int(items), st);
+            *grid = 0;                                     // nothing to join
+            return s;
+        }
+    }
+    return decode_stream<C, __nv_bfloat16>(pg::decode_tc<DK, DV, R, false>, ATTN_KERNEL_DECODE_TENSOR, C::kCtasPerSm,
+                                           a, Q, Kp, Vp, O, LSE, parts, grid, 0, st);
 }
 
 template <int DK, int DV, int RB, int R>
@@ -171,7 +201,7 @@ attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const
     a.tile_rows = RB * R;
     a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     return decode_stream<C, float>(pg::decode_f32<DK, DV, RB, R>, ATTN_KERNEL_DECODE_F32, 1, a, Q, Kp, Vp, O, LSE,
-                                   parts, grid, st);
+                                   parts, grid, 0, st);
 }
 
 // Query rows of an item: as many of a key head's as there are, up to 32 (bf16)
@@ -314,9 +344,10 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     else
         s = dv <= 64 ? decode_rows<128, 64>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, f32, st)
                      : decode_rows<128, 128>(a, Q, K_pages, V_pages, O, LSE, parts, &grid, f32, st);
-    if (s == ATTN_OK)
+    const bool join = grid > 0;
+    if (s == ATTN_OK && join)
         s = f32 ? decode_join<float>(a, O, LSE, parts, grid, st) : decode_join<__nv_bfloat16>(a, O, LSE, parts, grid, st);
-    if (s == ATTN_OK) g_last_launches = 2;
+    if (s == ATTN_OK) g_last_launches = join ? 2 : 1;
     return s;
 }
 

@@ -84,10 +84,20 @@ CASES = [
 ]
 
 
+# A long table row alone decides how a call is split: short rows and few items
+# are taken by teams of CTAs, one launch; else the split goes over all CTAs.
+SPLITS = pytest.mark.parametrize("room", [None, 5000], ids=["short_rows", "long_rows"])
+
+
+def width(lens, page, room):
+    return None if room is None else -(-max(room, *lens) // page) + 2
+
+
+@SPLITS
 @pytest.mark.parametrize("lens,H,Hkv,n,d,dv,page,causal,dt", CASES)
-def test_decode(lens, H, Hkv, n, d, dv, page, causal, dt):
+def test_decode(lens, H, Hkv, n, d, dv, page, causal, dt, room):
     rng = np.random.default_rng(len(lens) * 1000 + d + n)
-    dev, host = on_gpu(numpy_cache(rng, len(lens), Hkv, page, d, dv, lens), dt)
+    dev, host = on_gpu(numpy_cache(rng, len(lens), Hkv, page, d, dv, lens, M=width(lens, page, room)), dt)
     q = torch.tensor(rng.standard_normal((len(lens), H, n, d)), device="cuda").to(DT[dt])
     o, lse = run(dev, q, causal)
     compare(o, lse, dt, host, q, causal)
@@ -106,11 +116,12 @@ def test_split_and_joined(dt):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+@SPLITS
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_large_scores(dt):
+def test_large_scores(dt, room):
     """Scores of several hundred, of both signs of the scale, and a zero scale."""
     rng = np.random.default_rng(6)
-    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (400, 90)), dt)
+    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (400, 90), M=width((400,), 16, room)), dt)
     q = torch.tensor(20 * rng.standard_normal((2, 4, 2, 64)), device="cuda").to(DT[dt])
     for scale in (1.0, -1.0, 0.0):
         o, lse = run(dev, q, scale=scale)
@@ -119,10 +130,11 @@ def test_large_scores(dt):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [1, 4])
-def test_ragged_queries_leave_other_rows(dt, n):
+@SPLITS
+def test_ragged_queries_leave_other_rows(dt, n, room):
     rng = np.random.default_rng(7)
     lens, q_len = (70, 0, 200, 129, 3), (n, n, 0, max(1, n - 1), n)
-    dev, host = on_gpu(numpy_cache(rng, 5, 2, 8, 64, 64, lens), dt)
+    dev, host = on_gpu(numpy_cache(rng, 5, 2, 8, 64, 64, lens, M=width(lens, 8, room)), dt)
     q = torch.tensor(rng.standard_normal((5, 6, n, 64)), device="cuda").to(DT[dt])
     out = torch.full((5, 6, n, 64), 7.0, dtype=DT[dt], device="cuda")
     lse = torch.full((5, 6, n), 7.0, device="cuda")
@@ -135,12 +147,13 @@ def test_ragged_queries_leave_other_rows(dt, n):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("page", [8, 64])
-def test_unused_rows_have_no_influence(dt, page):
+@SPLITS
+def test_unused_rows_have_no_influence(dt, page, room):
     """NaN and infinities in every row that no token owns, free pages included,
     and table entries past the last page that lead nowhere."""
     rng = np.random.default_rng(8)
     lens = (1, 65, 131, 0)
-    c = numpy_cache(rng, 4, 2, page, 64, 64, lens)
+    c = numpy_cache(rng, 4, 2, page, 64, 64, lens, M=width(lens, page, room))
     q = torch.tensor(rng.standard_normal((4, 4, 3, 64)), device="cuda").to(DT[dt])
     dev, host = on_gpu(c, dt)
     want = run(dev, q)
@@ -161,12 +174,13 @@ def test_unused_rows_have_no_influence(dt, page):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("H", [2, 12])
-def test_later_tokens_of_a_draft_have_no_influence(dt, H):
+@SPLITS
+def test_later_tokens_of_a_draft_have_no_influence(dt, H, room):
     """An infinite or NaN key or value of a draft's last tokens reaches the
     queries that see it and no other."""
     rng = np.random.default_rng(9)
     lens, n = (64, 70, 8), 5
-    c = numpy_cache(rng, 3, 1, 16, 64, 64, lens)
+    c = numpy_cache(rng, 3, 1, 16, 64, 64, lens, M=width(lens, 16, room))
     q = torch.tensor(rng.standard_normal((3, H, n, 64)), device="cuda").to(DT[dt])
     dev, host = on_gpu(c, dt)
     want = run(dev, q)
@@ -242,13 +256,14 @@ def test_many_sequences():
     assert (run(dev, q, q_len=np.zeros(B, dtype=np.int32), out=out.clone().fill_(3))[0] == 3).all()
 
 
+@SPLITS
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_captured_streams_and_workspaces(dt):
+def test_captured_streams_and_workspaces(dt, room):
     """A captured call replayed on new inputs in place; calls at once on two
     streams with workspaces of their own; a workspace of any contents."""
     rng = np.random.default_rng(12)
     lens = (700, 20)
-    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, lens), dt)
+    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, lens, M=width(lens, 16, room)), dt)
     qs = [torch.tensor(rng.standard_normal((2, 4, 1, 64)), device="cuda").to(DT[dt]) for _ in range(2)]
     want = [run(dev, q) for q in qs]
     need = lib.attn_decode_workspace_size(2, 4, 2, 1, 64, 64, DT[dt])
