@@ -26,7 +26,12 @@ struct DecodeF32Cfg {
     static constexpr int kPanelCols = 32, kKPanels = DK / 32, kVPanels = DV / 32;
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
-    static constexpr int kStages = 192 * 1024 / kStageBytes;
+    // Two CTAs an SM where their stages fit: with 16 consumers instead of 8 the
+    // stream is busy (4 x 32768 tokens of 16 heads, d = 64: 165 us, 6.5 TB/s,
+    // against 237). At wider rows 16 consumers in one CTA, half of them on every
+    // other tile, gained nothing (197 us against 191).
+    static constexpr int kCtasPerSm = RB == 4 && DK == 64 && DV == 64 ? 2 : 1;
+    static constexpr int kStages = 192 / kCtasPerSm * 1024 / kStageBytes;
     static constexpr int kWarps = 8;                       // consumers: 8 / R key warps per group
     static constexpr int kKeyWarps = kWarps / R, kWarpKeys = kTileKeys / kKeyWarps;
     static constexpr int kThreads = (kWarps + 1) * 32;
@@ -38,7 +43,7 @@ struct DecodeF32Cfg {
 };
 
 template <int DK, int DV, int RB, int R>
-__global__ void __launch_bounds__(DecodeF32Cfg<DK, DV, RB, R>::kThreads, 1)
+__global__ void __launch_bounds__(DecodeF32Cfg<DK, DV, RB, R>::kThreads, DecodeF32Cfg<DK, DV, RB, R>::kCtasPerSm)
 decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DecodeArgs a,
            const float* __restrict__ Q, float* __restrict__ O, float* __restrict__ LSE, Parts parts,
            unsigned long long budget_ns) {

@@ -78,13 +78,12 @@ __device__ __forceinline__ void cluster_sync() {
 // and end. A sequence with queries and no keys has one (empty) tile per item,
 // so that its rows are written. Units are numbered sequence by sequence, item
 // by item, and every CTA takes the same number of consecutive ones, however
-// the lengths are spread, which the host does not know. An item cut by a CTA
+// the lengths are spread, which the host does not know. (64 sequences of 128 to
+// 16384 tokens: 173 us with kItemUnits = 0, 148 with 1, 145 with 2; 24 drafts of
+// 100 to 4000 tokens: 39, 30 and 28.) An item cut by a CTA
 // border is joined afterwards from its pieces.
 constexpr int kTileKeys = 64;
-#ifndef ITEM_UNITS
-#define ITEM_UNITS 2
-#endif
-constexpr int kItemUnits = ITEM_UNITS;
+constexpr int kItemUnits = 2;
 
 struct DecodeArgs {
     Geometry g;

@@ -200,7 +200,7 @@ attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const
     using C = pg::DecodeF32Cfg<DK, DV, RB, R>;
     a.tile_rows = RB * R;
     a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
-    return decode_stream<C, float>(pg::decode_f32<DK, DV, RB, R>, ATTN_KERNEL_DECODE_F32, 1, a, Q, Kp, Vp, O, LSE,
+    return decode_stream<C, float>(pg::decode_f32<DK, DV, RB, R>, ATTN_KERNEL_DECODE_F32, C::kCtasPerSm, a, Q, Kp, Vp, O, LSE,
                                    parts, grid, 0, st);
 }
 
