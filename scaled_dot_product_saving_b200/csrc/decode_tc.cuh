@@ -419,7 +419,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             const float Z = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) {
-                if (x[k].x == -INFINITY) continue;        // no keys there: its output was never written
+                if (x[k].y == 0.f) continue;              // no keys there: its output may not be written
                 const float f = ex2(x[k].x - Z);
                 L = fmaf(x[k].y, f, L);
                 y0 = fmaf(y[k].x, f, y0);

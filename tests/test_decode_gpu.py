@@ -334,3 +334,72 @@ def test_refusals():
     with pytest.raises(lib.AttnError) as e:
         lib.attn_decode(q, *args, out=q)
     assert e.value.code == 9
+
+
+@SPLITS
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_query_of_nan_stays_its_own(dt, room):
+    rng = np.random.default_rng(15)
+    lens = (130, 20)
+    dev, _ = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, lens, M=width(lens, 16, room)), dt)
+    q = torch.tensor(rng.standard_normal((2, 6, 2, 64)), device="cuda").to(DT[dt])
+    want = run(dev, q)
+    q[0, 1, 1, 5] = float("nan")
+    o, lse = run(dev, q)
+    other = torch.ones(2, 6, 2, dtype=torch.bool, device="cuda")
+    other[0, 1, 1] = False
+    assert torch.isnan(o[0, 1, 1]).all() and torch.isnan(lse[0, 1, 1])
+    assert torch.equal(o[other], want[0][other]) and torch.equal(lse[other], want[1][other])
+
+
+def test_launches_and_trace():
+    """What a call launches, as the library counts and traces it."""
+    rng = np.random.default_rng(16)
+    for dt, room, names in (("bf16", None, ["decode_tensor"]), ("bf16", 5000, ["decode_tensor", "decode_join"]),
+                            ("f32", None, ["decode_f32", "decode_join"])):
+        dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (90, 30), M=width((90,), 16, room)), dt)
+        q = torch.tensor(rng.standard_normal((2, 4, 1, 64)), device="cuda").to(DT[dt])
+        lib.attn_trace_begin(8)
+        try:
+            o, lse = run(dev, q)
+        finally:
+            trace = lib.attn_trace_end()
+        assert [name for name, _ in trace] == names
+        assert lib.attn_last_launch_count() == len(names)
+        compare(o, lse, dt, host, q)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_after_a_timeout_until_it_is_read(dt):
+    """While the error word is set a call returns and changes nothing outside its
+    outputs; once it has been read, calls work again."""
+    rng = np.random.default_rng(17)
+    for room in (None, 5000):
+        dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (90, 30), M=width((90,), 16, room)), dt)
+        q = torch.tensor(rng.standard_normal((2, 4, 1, 64)), device="cuda").to(DT[dt])
+        lib.attn_probe_timeout(1000)
+        lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"])
+        assert lib.attn_get_device_error() == lib.ATTN_ERR_DEVICE_TIMEOUT
+        o, lse = run(dev, q)
+        compare(o, lse, dt, host, q)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_shared_pages(dt):
+    """Sequences over the same pages, and one whose row repeats a page."""
+    rng = np.random.default_rng(18)
+    c = numpy_cache(rng, 3, 2, 16, 64, 64, (64, 64, 64))
+    c["table"][1, :3] = c["table"][0, :3]
+    c["table"][2, :4] = c["table"][2, 0]
+    dev, host = on_gpu(c, dt)
+    q = torch.tensor(rng.standard_normal((3, 4, 1, 64)), device="cuda").to(DT[dt])
+    compare(*run(dev, q), dt, host, q)
+
+
+def test_long_drafts():
+    """As many queries as a short prompt has: many items of query rows."""
+    rng = np.random.default_rng(19)
+    lens, n = (150, 100), 100
+    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, lens), "bf16")
+    q = torch.tensor(rng.standard_normal((2, 4, n, 64)), device="cuda").to(torch.bfloat16)
+    compare(*run(dev, q), "bf16", host, q)
