@@ -249,7 +249,8 @@ typedef enum {
     ATTN_KERNEL_CACHE_BOOKS = 15, /* table, lengths and counts of a cache call */
     ATTN_KERNEL_CACHE_ROWS = 16,  /* the rows that a cache call writes or moves */
     ATTN_KERNEL_DECODE_TENSOR = 17, /* tensor-core decode of bf16              */
-    ATTN_KERNEL_DECODE_F32 = 18   /* fp32 decode                               */
+    ATTN_KERNEL_DECODE_F32 = 18,  /* fp32 decode                               */
+    ATTN_KERNEL_DECODE_WIDE = 19  /* tcgen05 decode of bf16, many query rows   */
 } attn_kernel_id_t;
 
 typedef struct {

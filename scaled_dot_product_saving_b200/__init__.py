@@ -42,7 +42,7 @@ KERNEL_NAMES = {1: "fwd_tensor", 2: "fwd_simt", 3: "preprocess", 4: "bwd_tensor"
                 5: "bwd_simt", 6: "finalize", 7: "proj_gather", 8: "gemm",
                 9: "fwd_f32x", 10: "bwd_f32x", 11: "bwd_kv", 12: "bwd_dq",
                 13: "decode_simt", 14: "decode_join", 15: "cache_books", 16: "cache_rows",
-                17: "decode_tensor", 18: "decode_f32"}
+                17: "decode_tensor", 18: "decode_f32", 19: "decode_wide"}
 
 
 class _KernelTime(ctypes.Structure):

@@ -25,6 +25,7 @@
 #include "f32x_tc.cuh"
 #include "decode_tc.cuh"
 #include "decode_f32.cuh"
+#include "decode_wide.cuh"
 #include "cache.cuh"
 
 namespace {

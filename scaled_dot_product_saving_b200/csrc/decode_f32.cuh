@@ -58,7 +58,8 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     if (warp == C::kWarps) w.start(a);                     // while the barriers are set up
     if (!set_up<false>(parts, ring, smem, C::kWarps)) return;
     if (warp == C::kWarps) {
-        produce<C>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns);
+        produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns,
+                   [&](int row, int rows) { return prefetch_rows(Q, row, rows, a.d); });
         return;
     }
 

@@ -27,7 +27,7 @@ struct Stage {
     // with kFirst
     int row, rows;                   // first query row of the item in Q, O and LSE, and how many
     int i0;                          // the first row's query
-    int len, nq, t0;
+    int len, nq, t0, tiles;          // its first key tile, and how many
     int b, item, last;               // for the item's head: last, CTA of its last piece
 };
 
@@ -86,11 +86,12 @@ __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups
 
 // The producer warp. A tile is 64 / box pages (box = min(page, 64) tokens, one
 // lane each); 32 table entries are held across the warp and the next 32 are on
-// the way. C: the kernel's configuration.
-template <typename C, typename T, typename RingT, typename W>
+// the way. C: the kernel's configuration; begin(q_row, rows): called by the warp
+// when a piece begins, with its query rows, false to give up.
+template <typename C, typename RingT, typename W, typename F>
 __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMap* tmV, const DecodeArgs& a,
-                                        const T* Q, W& w, RingT& ring, uint8_t* smem,
-                                        unsigned long long budget_ns) {
+                                        W& w, RingT& ring, uint8_t* smem, unsigned long long budget_ns,
+                                        F&& begin) {
     constexpr int kStages = C::kStages;
     const int lane = threadIdx.x & 31;
     const int page_log2 = a.g.page_log2, page = 1 << page_log2;
@@ -107,10 +108,10 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
         const int hk = a.row_tiles == 1 ? p.item : p.item / a.row_tiles;
         const int r0 = (p.item - hk * a.row_tiles) * a.tile_rows, rows = min(a.tile_rows, a.rows - r0);
         const int q_row = int(row_base(a, p.b, hk)) + r0;
-        // The query rows, into L1 ahead of the warps that will read them.
-        const char* q = reinterpret_cast<const char*>(Q + size_t(q_row) * a.d);
-        for (int x = lane * 128; x < rows * a.d * int(sizeof(T)); x += 32 * 128)
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
+        if (!begin(q_row, rows)) {
+            going = false;
+            break;
+        }
         const int* row = a.table + size_t(p.b) * a.g.M;
         const int last = pages_of(p.len, page_log2);
         int base = (p.t0 * kTileKeys) >> page_log2;
@@ -152,6 +153,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                     st.len = p.len;
                     st.nq = p.nq;
                     st.t0 = p.t0;
+                    st.tiles = p.t1 - p.t0;
                     st.b = p.b;
                     st.item = p.item;
                     st.last = last_cta;
@@ -185,6 +187,15 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
     // stage that the end took was empty, and its barrier has moved on.)
     for (int x = max(0, n - kStages + (stopped ? 1 : 0)); x < n; ++x)
         (void)mbar_wait_timed(&ring.full[x % kStages], (x / kStages) & 1, budget_ns);
+}
+
+// The query rows into L1, ahead of the warps that will read them.
+template <typename T>
+__device__ __forceinline__ bool prefetch_rows(const T* Q, int q_row, int rows, int d) {
+    const char* q = reinterpret_cast<const char*>(Q + size_t(q_row) * d);
+    for (int x = (threadIdx.x & 31) * 128; x < rows * d * int(sizeof(T)); x += 32 * 128)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
+    return true;
 }
 
 // What a consumer keeps of the piece it is at.

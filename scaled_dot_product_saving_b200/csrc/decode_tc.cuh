@@ -390,7 +390,9 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     };
 
     if (warp == kKeyWarps * R) {
-        if (going) produce<C>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns);
+        if (going)
+            produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns,
+                   [&](int row, int rows) { return prefetch_rows(Q, row, rows, a.d); });
     } else if (going) {
         consume();
     }

@@ -6,10 +6,13 @@
 namespace {
 
 namespace pg = attn::paged;
+#ifndef WIDE
+#define WIDE 32
+#endif
 
-// Most CTAs of a decode call, and most CTAs times query rows of an item (32 rows
-// on one CTA an SM; 16 rows on up to three): what the workspace has slots for.
-constexpr int kDecodeCtas = 3 * 148, kDecodeRows = 48 * 148;
+// Most CTAs of a decode call, and most CTAs times query rows of an item: what the
+// workspace has slots for (one CTA an SM for items of 128 rows, up to three for 16).
+constexpr int kDecodeCtas = 3 * 148, kDecodeRows = 48 * 148, kDecodeWideRows = pg::kWideRows * 148;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -82,9 +85,9 @@ bool launch_dependent(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s
 struct DecodeWorkspace {
     size_t o_off, ml_off, head_off, total;
 };
-DecodeWorkspace carve_decode(int dv) {
+DecodeWorkspace carve_decode(int dv, long long rows_per_head) {
     DecodeWorkspace w;
-    const size_t rows = 2ull * kDecodeRows;
+    const size_t rows = 2ull * (rows_per_head > WIDE ? kDecodeWideRows : kDecodeRows);
     w.o_off = 0;
     w.ml_off = round_up(rows * dv * sizeof(float), 256);
     w.head_off = w.ml_off + round_up(rows * 2 * sizeof(float), 256);
@@ -135,10 +138,10 @@ attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg
 // The kernels that stream tiles with the TMA. C: the kernel's configuration; T:
 // the element type, whose columns the maps' 128-byte rows hold. teams: 0, or one
 // team for each of so many items.
-template <typename C, typename T, typename Kern>
+template <typename C, typename T, typename Kern, typename... More>
 attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg::DecodeArgs& a, const void* Q,
                             const void* Kp, const void* Vp, void* O, float* LSE, const pg::Parts& parts, int* grid,
-                            int teams, cudaStream_t st) {
+                            int teams, cudaStream_t st, const More&... more) {
     CUtensorMap mk, mv;
     const int page = 1 << a.g.page_log2, heads = a.g.P * a.g.Hkv, box = std::min(page, pg::kTileKeys);
     constexpr auto type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -148,7 +151,7 @@ attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg:
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
         return ATTN_ERR_CUDA;
     *grid = teams > 0 ? teams * pg::kTeam
-                      : std::min(ctas_per_sm * sm_count(), std::min(kDecodeCtas, kDecodeRows / a.tile_rows));
+                      : std::min(ctas_per_sm * sm_count(), std::min(kDecodeCtas, a.tile_rows == pg::kWideRows ? 148 : kDecodeRows / a.tile_rows));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(*grid);
     cfg.blockDim = dim3(C::kThreads);
@@ -163,7 +166,7 @@ attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg:
     cfg.numAttrs = teams > 0 ? 1 : 0;
     return traced(kernel_id, st, [&] {
         if (cudaLaunchKernelEx(&cfg, kern, mk, mv, a, static_cast<const T*>(Q), static_cast<T*>(O), LSE, parts,
-                               kWaitBudgetNs) != cudaSuccess) {
+                               kWaitBudgetNs, more...) != cudaSuccess) {
             (void)cudaGetLastError();
             return ATTN_ERR_CUDA;
         }
@@ -194,6 +197,19 @@ attn_status_t decode_tc(pg::DecodeArgs& a, const void* Q, const void* Kp, const 
                                            a, Q, Kp, Vp, O, LSE, parts, grid, 0, st);
 }
 
+template <int DK, int DV>
+attn_status_t decode_wide(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
+                          const pg::Parts& parts, int* grid, cudaStream_t st) {
+    using C = pg::DecodeWideCfg<DK, DV>;
+    a.tile_rows = pg::kWideRows;
+    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
+    CUtensorMap mq;
+    if (!make_map_rows(&mq, Q, a.d, a.g.B * a.H * a.n, a.d, 64, pg::kWideRows)) return ATTN_ERR_CUDA;
+    return decode_stream<C, __nv_bfloat16>(pg::decode_wide<DK, DV>, ATTN_KERNEL_DECODE_WIDE, 1, a, Q, Kp, Vp, O, LSE,
+                                           parts, grid, 0, st, mq, static_cast<const __nv_bfloat16*>(Kp),
+                                           static_cast<const __nv_bfloat16*>(Vp));
+}
+
 template <int DK, int DV, int RB, int R>
 attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                          const pg::Parts& parts, int* grid, cudaStream_t st) {
@@ -215,7 +231,8 @@ attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, cons
         return decode_f32<DK, DV, 8, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
     }
     if (a.rows <= 16) return decode_tc<DK, DV, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
-    return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    if (a.rows <= WIDE) return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    return decode_wide<DK, DV>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
 }
 
 // ------------------------------------------------------------------- books
@@ -294,7 +311,7 @@ extern "C" {
 
 size_t attn_decode_workspace_size(int B, int H, int Hkv, int n, int d, int dv, attn_dtype_t dtype) {
     if (check_decode(B, H, Hkv, n, d, dv, dtype) != ATTN_OK) return 0;
-    return carve_decode(dv).total;
+    return carve_decode(dv, 1ll * H / Hkv * n).total;
 }
 
 attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_pages, const int* table,
@@ -311,7 +328,7 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O) || !aligned16(LSE) ||
         !aligned4(table) || !aligned4(lens) || !aligned4(q_len))
         return ATTN_ERR_ALIGN;
-    const DecodeWorkspace w = carve_decode(dv);
+    const DecodeWorkspace w = carve_decode(dv, 1ll * H / Hkv * n);
     if (!workspace || workspace_bytes < w.total) return ATTN_ERR_WORKSPACE;
     if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
 

@@ -75,6 +75,10 @@ CASES = [
     ((150, 0, 70), 72, 1, 1, 128, 128, 16, True, "bf16"),            # more rows than one item takes
     ((150, 3, 70), 30, 2, 5, 64, 128, 16, True, "bf16"),             # 75 rows, the last item nearly empty
     ((150, 3, 70), 26, 2, 4, 128, 64, 32, True, "bf16"),
+    ((700, 64, 1, 0, 130), 40, 1, 1, 128, 128, 16, True, "bf16"),    # one to eleven key tiles; none
+    ((400, 65), 16, 1, 8, 64, 64, 64, True, "bf16"),                 # 128 rows
+    ((400, 65), 17, 1, 8, 128, 64, 8, False, "bf16"),                # 136: a second item of 8
+    ((129, 300), 36, 1, 1, 72, 40, 256, True, "bf16"),               # odd widths
     ((1,), 2, 1, 1, 64, 64, 16, True, "f32"),
     ((0, 1, 63, 64, 65, 129), 8, 2, 1, 128, 128, 16, True, "f32"),
     ((700, 129), 20, 4, 1, 64, 64, 16, True, "f32"),
@@ -103,13 +107,13 @@ def test_decode(lens, H, Hkv, n, d, dv, page, causal, dt, room):
     compare(o, lse, dt, host, q, causal)
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_split_and_joined(dt):
+@pytest.mark.parametrize("dt,H", [("bf16", 8), ("bf16", 48), ("bf16", 100), ("f32", 8), ("f32", 16), ("f32", 40)])
+def test_split_and_joined(dt, H):
     """Lengths far apart: the long sequence is cut over many CTAs."""
     rng = np.random.default_rng(5)
     lens = (9000, 3, 130, 0, 2500)
     dev, host = on_gpu(numpy_cache(rng, 5, 2, 16, 64, 64, lens), dt)
-    q = torch.tensor(rng.standard_normal((5, 8, 1, 64)), device="cuda").to(DT[dt])
+    q = torch.tensor(rng.standard_normal((5, H, 1, 64)), device="cuda").to(DT[dt])
     o, lse = run(dev, q)
     compare(o, lse, dt, host, q)
     again = run(dev, q)
@@ -117,19 +121,19 @@ def test_split_and_joined(dt):
 
 
 @SPLITS
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_large_scores(dt, room):
+@pytest.mark.parametrize("dt,H", [("bf16", 4), ("bf16", 40), ("f32", 4)])
+def test_large_scores(dt, H, room):
     """Scores of several hundred, of both signs of the scale, and a zero scale."""
     rng = np.random.default_rng(6)
     dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (400, 90), M=width((400,), 16, room)), dt)
-    q = torch.tensor(20 * rng.standard_normal((2, 4, 2, 64)), device="cuda").to(DT[dt])
+    q = torch.tensor(20 * rng.standard_normal((2, H, 2, 64)), device="cuda").to(DT[dt])
     for scale in (1.0, -1.0, 0.0):
         o, lse = run(dev, q, scale=scale)
         compare(o, lse, dt, host, q, scale=scale)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("n", [1, 4, 15])
 @SPLITS
 def test_ragged_queries_leave_other_rows(dt, n, room):
     rng = np.random.default_rng(7)
@@ -147,14 +151,15 @@ def test_ragged_queries_leave_other_rows(dt, n, room):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("page", [8, 64])
+@pytest.mark.parametrize("H", [4, 24])
 @SPLITS
-def test_unused_rows_have_no_influence(dt, page, room):
+def test_unused_rows_have_no_influence(dt, page, H, room):
     """NaN and infinities in every row that no token owns, free pages included,
     and table entries past the last page that lead nowhere."""
     rng = np.random.default_rng(8)
     lens = (1, 65, 131, 0)
     c = numpy_cache(rng, 4, 2, page, 64, 64, lens, M=width(lens, page, room))
-    q = torch.tensor(rng.standard_normal((4, 4, 3, 64)), device="cuda").to(DT[dt])
+    q = torch.tensor(rng.standard_normal((4, H, 3, 64)), device="cuda").to(DT[dt])
     dev, host = on_gpu(c, dt)
     want = run(dev, q)
     compare(*want, dt, host, q)
@@ -173,7 +178,7 @@ def test_unused_rows_have_no_influence(dt, page, room):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("H", [2, 12])
+@pytest.mark.parametrize("H", [2, 12, 20])
 @SPLITS
 def test_later_tokens_of_a_draft_have_no_influence(dt, H, room):
     """An infinite or NaN key or value of a draft's last tokens reaches the
@@ -201,8 +206,8 @@ def test_later_tokens_of_a_draft_have_no_influence(dt, H, room):
             assert torch.isfinite(o[..., rest]).all() and torch.equal(lse, want[1])
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_bad_page_numbers_and_lengths(dt):
+@pytest.mark.parametrize("dt,H", [("bf16", 4), ("bf16", 44), ("f32", 4)])
+def test_bad_page_numbers_and_lengths(dt, H):
     """Page numbers outside the pool mask their tokens; lengths are clamped."""
     rng = np.random.default_rng(10)
     c = numpy_cache(rng, 3, 2, 16, 64, 64, (100, 100, 100), M=7)
@@ -211,7 +216,7 @@ def test_bad_page_numbers_and_lengths(dt):
     c["table"][1, :7] = -1                                 # nothing left: an empty row
     c["lens"] = np.array([100, 100, -5], dtype=np.int32)
     dev, host = on_gpu(c, dt)
-    q = torch.tensor(rng.standard_normal((3, 4, 2, 64)), device="cuda").to(DT[dt])
+    q = torch.tensor(rng.standard_normal((3, H, 2, 64)), device="cuda").to(DT[dt])
     compare(*run(dev, q), dt, host, q)
     c["lens"] = np.array([2 ** 31 - 1, 5, 1000], dtype=np.int32)     # the row holds 112
     c["table"][2, 6] = 0
@@ -337,16 +342,16 @@ def test_refusals():
 
 
 @SPLITS
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_a_query_of_nan_stays_its_own(dt, room):
+@pytest.mark.parametrize("dt,H", [("bf16", 6), ("bf16", 40), ("f32", 6)])
+def test_a_query_of_nan_stays_its_own(dt, H, room):
     rng = np.random.default_rng(15)
     lens = (130, 20)
     dev, _ = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, lens, M=width(lens, 16, room)), dt)
-    q = torch.tensor(rng.standard_normal((2, 6, 2, 64)), device="cuda").to(DT[dt])
+    q = torch.tensor(rng.standard_normal((2, H, 2, 64)), device="cuda").to(DT[dt])
     want = run(dev, q)
     q[0, 1, 1, 5] = float("nan")
     o, lse = run(dev, q)
-    other = torch.ones(2, 6, 2, dtype=torch.bool, device="cuda")
+    other = torch.ones(2, H, 2, dtype=torch.bool, device="cuda")
     other[0, 1, 1] = False
     assert torch.isnan(o[0, 1, 1]).all() and torch.isnan(lse[0, 1, 1])
     assert torch.equal(o[other], want[0][other]) and torch.equal(lse[other], want[1][other])
@@ -355,10 +360,11 @@ def test_a_query_of_nan_stays_its_own(dt, room):
 def test_launches_and_trace():
     """What a call launches, as the library counts and traces it."""
     rng = np.random.default_rng(16)
-    for dt, room, names in (("bf16", None, ["decode_tensor"]), ("bf16", 5000, ["decode_tensor", "decode_join"]),
-                            ("f32", None, ["decode_f32", "decode_join"])):
+    for dt, room, H, names in (("bf16", None, 4, ["decode_tensor"]), ("bf16", 5000, 4, ["decode_tensor", "decode_join"]),
+                               ("bf16", None, 80, ["decode_wide", "decode_join"]),
+                               ("f32", None, 4, ["decode_f32", "decode_join"])):
         dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (90, 30), M=width((90,), 16, room)), dt)
-        q = torch.tensor(rng.standard_normal((2, 4, 1, 64)), device="cuda").to(DT[dt])
+        q = torch.tensor(rng.standard_normal((2, H, 1, 64)), device="cuda").to(DT[dt])
         lib.attn_trace_begin(8)
         try:
             o, lse = run(dev, q)
@@ -374,9 +380,9 @@ def test_after_a_timeout_until_it_is_read(dt):
     """While the error word is set a call returns and changes nothing outside its
     outputs; once it has been read, calls work again."""
     rng = np.random.default_rng(17)
-    for room in (None, 5000):
+    for room, H in ((None, 4), (5000, 4), (None, 80)):
         dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (90, 30), M=width((90,), 16, room)), dt)
-        q = torch.tensor(rng.standard_normal((2, 4, 1, 64)), device="cuda").to(DT[dt])
+        q = torch.tensor(rng.standard_normal((2, H, 1, 64)), device="cuda").to(DT[dt])
         lib.attn_probe_timeout(1000)
         lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"])
         assert lib.attn_get_device_error() == lib.ATTN_ERR_DEVICE_TIMEOUT
