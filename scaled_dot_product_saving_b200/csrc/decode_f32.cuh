@@ -59,7 +59,7 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     if (!set_up<false>(parts, ring, smem, C::kWarps)) return;
     if (warp == C::kWarps) {
         produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns,
-                   [&](int row, int rows) { return prefetch_rows(Q, row, rows, a.d); });
+                   [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); });
         return;
     }
 

@@ -39,11 +39,23 @@ struct Ring {
     int abort;
 };
 
-// False once the call is being abandoned.
+// Warp-wide wait; false once the call is being abandoned. The bound is counted
+// with the SM's clock: reading the global timer costs some thousand cycles, which
+// every wait that does not succeed at once would pay.
 template <typename RingT>
 __device__ __forceinline__ bool ring_wait(RingT& ring, uint64_t* bar, uint32_t parity, unsigned long long budget_ns) {
     volatile int* abort = &ring.abort;
-    if (mbar_wait_warp(bar, parity, abort, budget_ns)) return true;
+    const uint32_t at = smem_addr(bar);
+    bool ok = mbar_try_wait(at, parity);
+    if (!ok) {
+        const long long from = clock64();
+        for (uint32_t turn = 1; !ok; ++turn) {
+            ok = mbar_try_wait(at, parity);
+            // Two cycles a nanosecond: no SM clock is above 2 GHz.
+            if (!ok && (turn & 15u) == 0u && (*abort || (unsigned long long)(clock64() - from) > 2 * budget_ns)) break;
+        }
+    }
+    if (__all_sync(0xffffffffu, ok)) return true;
     if (*abort == 0) {
         record_device_error(kErrTimeout);
         *abort = 1;
@@ -86,8 +98,8 @@ __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups
 
 // The producer warp. A tile is 64 / box pages (box = min(page, 64) tokens, one
 // lane each); 32 table entries are held across the warp and the next 32 are on
-// the way. C: the kernel's configuration; begin(q_row, rows): called by the warp
-// when a piece begins, with its query rows, false to give up.
+// the way. C: the kernel's configuration; begin(piece): called by the warp
+// when a piece begins, with its description, false to give up.
 template <typename C, typename RingT, typename W, typename F>
 __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMap* tmV, const DecodeArgs& a,
                                         W& w, RingT& ring, uint8_t* smem, unsigned long long budget_ns,
@@ -106,9 +118,21 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
     Piece p;
     while (going && w.next(a, &p)) {
         const int hk = a.row_tiles == 1 ? p.item : p.item / a.row_tiles;
-        const int r0 = (p.item - hk * a.row_tiles) * a.tile_rows, rows = min(a.tile_rows, a.rows - r0);
-        const int q_row = int(row_base(a, p.b, hk)) + r0;
-        if (!begin(q_row, rows)) {
+        const int r0 = (p.item - hk * a.row_tiles) * a.tile_rows;
+        Stage d;
+        d.present = 0;
+        d.flags = kFirst | (p.t0 == 0 ? kStarts : 0) | (p.t1 == p.tiles ? kEnds : 0);
+        d.row = int(row_base(a, p.b, hk)) + r0;
+        d.rows = min(a.tile_rows, a.rows - r0);
+        d.i0 = a.n == 1 ? 0 : r0 % a.n;
+        d.len = p.len;
+        d.nq = p.nq;
+        d.t0 = p.t0;
+        d.tiles = p.t1 - p.t0;
+        d.b = p.b;
+        d.item = p.item;
+        d.last = (d.flags & kStarts) && !(d.flags & kEnds) ? w.owner(p.end - 1) : 0;
+        if (!begin(d)) {
             going = false;
             break;
         }
@@ -117,7 +141,6 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
         int base = (p.t0 * kTileKeys) >> page_log2;
         int held = base + lane < last ? row[base + lane] : -1;
         int ahead = base + 32 + lane < last ? row[base + 32 + lane] : -1;
-        const int last_cta = p.t0 == 0 && p.t1 < p.tiles ? w.owner(p.end - 1) : 0;
         for (int t = p.t0; t < p.t1; ++t, ++n) {
             const int k0 = t * kTileKeys, first = k0 >> page_log2;
             if (first - base >= 32) {
@@ -143,22 +166,9 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                 }
                 if (p.len - k0 < kTileKeys) keys &= p.len > k0 ? (1ull << (p.len - k0)) - 1ull : 0ull;
                 Stage& st = ring.stage[s];
+                if (t == p.t0) st = d;
                 st.present = keys;
-                int flags = t == p.t1 - 1 ? kLast : 0;
-                if (t == p.t0) {
-                    flags |= kFirst | (p.t0 == 0 ? kStarts : 0) | (p.t1 == p.tiles ? kEnds : 0);
-                    st.row = q_row;
-                    st.rows = rows;
-                    st.i0 = a.n == 1 ? 0 : r0 % a.n;
-                    st.len = p.len;
-                    st.nq = p.nq;
-                    st.t0 = p.t0;
-                    st.tiles = p.t1 - p.t0;
-                    st.b = p.b;
-                    st.item = p.item;
-                    st.last = last_cta;
-                }
-                st.flags = flags;
+                st.flags = (t == p.t0 ? d.flags : 0) | (t == p.t1 - 1 ? kLast : 0);
                 mbar_arrive_expect_tx(&ring.full[s], __popc(loads) * box * (C::kKPanels + C::kVPanels) * 128);
             }
             __syncwarp();

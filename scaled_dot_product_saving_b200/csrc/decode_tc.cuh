@@ -392,7 +392,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     if (warp == kKeyWarps * R) {
         if (going)
             produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns,
-                   [&](int row, int rows) { return prefetch_rows(Q, row, rows, a.d); });
+                   [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); });
     } else if (going) {
         consume();
     }
