@@ -268,36 +268,40 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                     tmem_ld_wait(s1);
                     // The extreme raw score, then scaled: the least for a scale below zero.
                     uint32_t lo = ~0u, hi = ~0u;             // keys that exist and that this row sees
-                    const uint32_t worst = __float_as_uint(scale_log2 < 0.f ? INFINITY : -INFINITY);
                     if (!whole) {
                         const int left = see - k0;
                         const unsigned long long seen =
                             present & (left >= kTileKeys ? ~0ull : left > 0 ? (1ull << left) - 1ull : 0ull);
                         lo = uint32_t(seen);
                         hi = uint32_t(seen >> 32);
+                        const uint32_t worst = __float_as_uint(scale_log2 < 0.f ? INFINITY : -INFINITY);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             if (!(lo >> e & 1)) s0[e] = worst;
                             if (!(hi >> e & 1)) s1[e] = worst;
                         }
                     }
-                    float t0 = __uint_as_float(worst), t1 = t0;
+                    float t[4];
                     if (scale_log2 < 0.f) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            t0 = fmin3(t0, __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
-                            t1 = fmin3(t1, __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
-                        }
-                        t0 = fminf(t0, t1);
-                    } else {
+                        for (int e = 0; e < 4; ++e) t[e] = INFINITY;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            t0 = fmax3(t0, __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
-                            t1 = fmax3(t1, __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
+                            t[e & 2] = fmin3(t[e & 2], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
+                            t[(e & 2) + 1] = fmin3(t[(e & 2) + 1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
                         }
-                        t0 = fmaxf(t0, t1);
+                        t[0] = fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) t[e] = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            t[e & 2] = fmax3(t[e & 2], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
+                            t[(e & 2) + 1] = fmax3(t[(e & 2) + 1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
+                        }
+                        t[0] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                     }
-                    const float top = (lo | hi) != 0 ? t0 * scale_log2 : -INFINITY;
+                    const float top = (lo | hi) != 0 ? t[0] * scale_log2 : -INFINITY;
                     // The reference value moves, and O is rescaled, only when the
                     // maximum has grown by more than 8 (base 2).
                     const bool want = top > m_run + 8.f;
@@ -323,27 +327,35 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                         }
                     }
                     const float z = m_run == -INFINITY ? 0.f : m_run;
-                    float sum0 = 0.f, sum1 = 0.f;
+                    f32x2 sum = make_f32x2(0.f, 0.f);
+                    const f32x2 sl2 = make_f32x2(scale_log2, scale_log2), nz2 = make_f32x2(-z, -z);
                     // Weights in bf16 for the second product (half a step, 2^-8 of
                     // each), over the scores; their sum is of the unrounded ones.
-                    auto half_tile = [&](const uint32_t(&sc)[32], uint32_t seen, uint32_t to) {
+                    auto half_tile = [&](const uint32_t(&sc)[32], uint32_t seen, uint32_t to, auto masked) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float q0 = ex2(fmaf(__uint_as_float(sc[2 * e]), scale_log2, -z));
-                            float q1 = ex2(fmaf(__uint_as_float(sc[2 * e + 1]), scale_log2, -z));
-                            if (!whole) {
+                            const float2 y = split_f32x2(fma_x2(
+                                make_f32x2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sl2, nz2));
+                            float q0 = ex2(y.x), q1 = ex2(y.y);
+                            if constexpr (decltype(masked)::value) {
                                 if (!(seen >> (2 * e) & 1)) q0 = 0.f;
                                 if (!(seen >> (2 * e + 1) & 1)) q1 = 0.f;
                             }
-                            sum0 += q0;
-                            sum1 += q1;
+                            sum = add_x2(sum, make_f32x2(q0, q1));
                             pk[e] = pack_bf16x2(q0, q1);
                         }
                         tmem_st16(to, pk);
                     };
-                    half_tile(s0, lo, tS);
-                    half_tile(s1, hi, tS + 16);
+                    if (whole) {
+                        half_tile(s0, lo, tS, std::false_type{});
+                        half_tile(s1, hi, tS + 16, std::false_type{});
+                    } else {
+                        half_tile(s0, lo, tS, std::true_type{});
+                        half_tile(s1, hi, tS + 16, std::true_type{});
+                    }
+                    const float2 both_sums = split_f32x2(sum);
+                    const float sum0 = both_sums.x, sum1 = both_sums.y;
                     l_run += sum0 + sum1;
                     tmem_st_wait();
                 }
