@@ -226,8 +226,10 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             float m_run = -INFINITY, l_run = 0.f;
             for (int i = x; ok && i < tiles; i += 2) {
                 const int g = g0 + i, b = g & 3, s = g % kStages, k0 = first_key + i * kTileKeys;
-                ok = ring_wait(ring, &ring.full[s], (g / kStages) & 1, budget_ns) &&
-                     ring_wait(ring, &bars.s_full[b], (g >> 2) & 1, budget_ns);
+                // The second wait is over as soon as it begins: it is for what was
+                // written beside the tile, and for V where it is mended below.
+                ok = ring_wait(ring, &bars.s_full[b], (g >> 2) & 1, budget_ns) &&
+                     ring_wait(ring, &ring.full[s], (g / kStages) & 1, budget_ns);
                 if (!ok) break;
                 tc_fence_after();
                 const unsigned long long present = ring.stage[s].present;
@@ -266,7 +268,6 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                     tmem_ld32(tS + 32, s1);
                     tmem_ld_wait(s0);
                     tmem_ld_wait(s1);
-                    // The extreme raw score, then scaled: the least for a scale below zero.
                     uint32_t lo = ~0u, hi = ~0u;             // keys that exist and that this row sees
                     if (!whole) {
                         const int left = see - k0;
@@ -274,6 +275,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                             present & (left >= kTileKeys ? ~0ull : left > 0 ? (1ull << left) - 1ull : 0ull);
                         lo = uint32_t(seen);
                         hi = uint32_t(seen >> 32);
+                        // Scaled scores of the others are -inf below, whatever they hold.
                         const uint32_t worst = __float_as_uint(scale_log2 < 0.f ? INFINITY : -INFINITY);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
@@ -281,82 +283,72 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                             if (!(hi >> e & 1)) s1[e] = worst;
                         }
                     }
-                    float t[4];
-                    if (scale_log2 < 0.f) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) t[e] = INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            t[e & 2] = fmin3(t[e & 2], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
-                            t[(e & 2) + 1] = fmin3(t[(e & 2) + 1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
-                        }
-                        t[0] = fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) t[e] = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            t[e & 2] = fmax3(t[e & 2], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
-                            t[(e & 2) + 1] = fmax3(t[(e & 2) + 1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
-                        }
-                        t[0] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                    }
-                    const float top = (lo | hi) != 0 ? t[0] * scale_log2 : -INFINITY;
-                    // The reference value moves, and O is rescaled, only when the
-                    // maximum has grown by more than 8 (base 2).
-                    const bool want = top > m_run + 8.f;
-                    const bool rescale = __any_sync(0xffffffffu, want && i >= 2);
-                    float alpha = 1.f;
-                    if (want) {
-                        alpha = ex2(m_run - top);
-                        m_run = top;
-                        l_run *= alpha;
-                    }
-                    if (rescale) {
-                        // The stream's last product must have left O.
-                        ok = ring_wait(ring, &bars.pv_done[(g - 2) & 3], ((g - 2) >> 2) & 1, budget_ns);
-                        tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < DV / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + DV * x + 32 * c, o);
-                            tmem_ld_wait(o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(tO + DV * x + 32 * c, o);
-                        }
-                    }
-                    const float z = m_run == -INFINITY ? 0.f : m_run;
-                    f32x2 sum = make_f32x2(0.f, 0.f);
-                    const f32x2 sl2 = make_f32x2(scale_log2, scale_log2), nz2 = make_f32x2(-z, -z);
-                    // Weights in bf16 for the second product (half a step, 2^-8 of
-                    // each), over the scores; their sum is of the unrounded ones.
-                    auto half_tile = [&](const uint32_t(&sc)[32], uint32_t seen, uint32_t to, auto masked) {
-                        uint32_t pk[16];
+                    // Weights against the reference value as it is, in bf16 for the
+                    // second product (half a step, 2^-8 of each); their sum is of the
+                    // unrounded ones, and the extreme raw score is found on the way.
+                    const f32x2 sl2 = make_f32x2(scale_log2, scale_log2);
+                    const bool falling = scale_log2 < 0.f;
+                    uint32_t pk[32];
+                    float sum = 0.f, far = falling ? INFINITY : -INFINITY;
+                    auto weigh = [&](const uint32_t(&sc)[32], uint32_t seen, uint32_t* to, f32x2 nz2, f32x2& acc, auto masked) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float2 y = split_f32x2(fma_x2(
-                                make_f32x2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sl2, nz2));
+                            const float a0 = __uint_as_float(sc[2 * e]), a1 = __uint_as_float(sc[2 * e + 1]);
+                            const float2 y = split_f32x2(fma_x2(make_f32x2(a0, a1), sl2, nz2));
                             float q0 = ex2(y.x), q1 = ex2(y.y);
                             if constexpr (decltype(masked)::value) {
                                 if (!(seen >> (2 * e) & 1)) q0 = 0.f;
                                 if (!(seen >> (2 * e + 1) & 1)) q1 = 0.f;
                             }
-                            sum = add_x2(sum, make_f32x2(q0, q1));
-                            pk[e] = pack_bf16x2(q0, q1);
+                            far = falling ? fmin3(far, a0, a1) : fmax3(far, a0, a1);
+                            acc = add_x2(acc, make_f32x2(q0, q1));
+                            to[e] = pack_bf16x2(q0, q1);
                         }
-                        tmem_st16(to, pk);
                     };
-                    if (whole) {
-                        half_tile(s0, lo, tS, std::false_type{});
-                        half_tile(s1, hi, tS + 16, std::false_type{});
-                    } else {
-                        half_tile(s0, lo, tS, std::true_type{});
-                        half_tile(s1, hi, tS + 16, std::true_type{});
+                    auto weigh_all = [&](float z) {
+                        const f32x2 nz2 = make_f32x2(-z, -z);
+                        f32x2 u = make_f32x2(0.f, 0.f), v = u;
+                        if (whole) {
+                            weigh(s0, lo, pk, nz2, u, std::false_type{});
+                            weigh(s1, hi, pk + 16, nz2, v, std::false_type{});
+                        } else {
+                            weigh(s0, lo, pk, nz2, u, std::true_type{});
+                            weigh(s1, hi, pk + 16, nz2, v, std::true_type{});
+                        }
+                        const float2 w = split_f32x2(add_x2(u, v));
+                        sum = w.x + w.y;
+                    };
+                    weigh_all(m_run == -INFINITY ? 0.f : m_run);
+                    const float top = (lo | hi) != 0 ? far * scale_log2 : -INFINITY;
+                    // The reference value moves, and O is rescaled, only when the
+                    // maximum has grown by more than 8 (base 2): on a piece's first tile
+                    // and rarely after it. The weights are then taken again.
+                    const bool want = top > m_run + 8.f;
+                    if (__any_sync(0xffffffffu, want)) {
+                        float alpha = 1.f;
+                        if (want) {
+                            alpha = ex2(m_run - top);
+                            m_run = top;
+                            l_run *= alpha;
+                        }
+                        if (i >= 2) {
+                            // The stream's last product must have left O.
+                            ok = ring_wait(ring, &bars.pv_done[(g - 2) & 3], ((g - 2) >> 2) & 1, budget_ns);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < DV; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + DV * x + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(tO + DV * x + c, o);
+                            }
+                        }
+                        weigh_all(m_run == -INFINITY ? 0.f : m_run);
                     }
-                    const float2 both_sums = split_f32x2(sum);
-                    const float sum0 = both_sums.x, sum1 = both_sums.y;
-                    l_run += sum0 + sum1;
+                    tmem_st32(tS, pk);
+                    l_run += sum;
                     tmem_st_wait();
                 }
                 tc_fence_before();
