@@ -34,7 +34,8 @@ struct DecodeF32Cfg {
     static constexpr int kStages = 192 / kCtasPerSm * 1024 / kStageBytes;
     static constexpr int kWarps = 8;                       // consumers: 8 / R key warps per group
     static constexpr int kKeyWarps = kWarps / R, kWarpKeys = kTileKeys / kKeyWarps;
-    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kProducers = kCtasPerSm == 1 ? 2 : 1;
+    static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kTileRows = RB * R;
     // The warps' outputs, when a piece ends, lie in the stage of its last tile.
     static_assert(kWarps * RB * DV * 4 <= kStageBytes, "outputs larger than a stage");
@@ -55,11 +56,13 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     Walker w;
-    if (warp == C::kWarps) w.start(a);                     // while the barriers are set up
-    if (!set_up<false>(parts, ring, smem, C::kWarps)) return;
-    if (warp == C::kWarps) {
-        produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns,
-                   [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); });
+    if (warp >= C::kWarps) w.start(a);                     // while the barriers are set up
+    if (!set_up<false>(parts, ring, smem, C::kWarps, C::kProducers)) return;
+    if (warp >= C::kWarps) {
+        auto begin = [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); };
+        if (C::kProducers == 1) produce<C, Loads::kBoth>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
+        else if (warp == C::kWarps) produce<C, Loads::kKeys>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
+        else produce<C, Loads::kValues>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
         return;
     }
 

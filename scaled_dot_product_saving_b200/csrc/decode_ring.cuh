@@ -73,14 +73,14 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 // timeout has not been read, in which case the call does nothing.
 template <bool kTeamed, int kStages, int kGroups>
 __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups>& ring, const uint8_t* smem,
-                                       int consumers) {
+                                       int consumers, int producers) {
     if (threadIdx.x == 0) {
         if (!kTeamed) parts.head[blockIdx.x].b = -1;
         const bool misaligned = (smem_addr(smem) & 1023u) != 0;
         if (misaligned) record_device_error(kErrTimeout);
         ring.abort = misaligned || *reinterpret_cast<volatile unsigned int*>(&g_device_error) != 0;
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&ring.full[s], 1);
+            mbar_init(&ring.full[s], producers);
             mbar_init(&ring.empty[s], consumers);
         }
         for (int x = 0; x < kGroups; ++x) {
@@ -96,15 +96,24 @@ __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups
     return !skip;
 }
 
-// The producer warp. A tile is 64 / box pages (box = min(page, 64) tokens, one
+// What a producer warp loads. One warp issues a copy in about 100 cycles, and a
+// tile of small pages takes many (16 of 16 tokens at d = 128): where a CTA has
+// an SM to itself, K and V have a warp each (8 sequences of 17000 tokens, 20
+// query rows, pages of 16: 123 us with one, 107
+// with two; in fp32, 4 rows of 32768 tokens, 191 and 167).
+enum class Loads { kBoth, kKeys, kValues };
+
+// A producer warp; the one of K, or of both, leads. A tile is 64 / box pages (box = min(page, 64) tokens, one
 // lane each); 32 table entries are held across the warp and the next 32 are on
 // the way. C: the kernel's configuration; begin(piece): called by the warp
 // when a piece begins, with its description, false to give up.
-template <typename C, typename RingT, typename W, typename F>
+template <typename C, Loads kLoads, typename RingT, typename W, typename F>
 __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMap* tmV, const DecodeArgs& a,
                                         W& w, RingT& ring, uint8_t* smem, unsigned long long budget_ns,
                                         F&& begin) {
     constexpr int kStages = C::kStages;
+    constexpr bool kLead = kLoads != Loads::kValues;
+    constexpr int kK = kLoads != Loads::kValues ? C::kKPanels : 0, kV = kLoads != Loads::kKeys ? C::kVPanels : 0;
     const int lane = threadIdx.x & 31;
     const int page_log2 = a.g.page_log2, page = 1 << page_log2;
     const int box_log2 = min(page_log2, 6), box = 1 << box_log2, boxes = kTileKeys >> box_log2;
@@ -132,7 +141,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
         d.b = p.b;
         d.item = p.item;
         d.last = (d.flags & kStarts) && !(d.flags & kEnds) ? w.owner(p.end - 1) : 0;
-        if (!begin(d)) {
+        if (kLead && !begin(d)) {
             going = false;
             break;
         }
@@ -157,29 +166,31 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                 break;
             }
             if (lane == 0) {
-                unsigned long long keys = ~0ull;
-                if (loads != (1u << boxes) - 1u) {
-                    const unsigned long long one = box == 64 ? ~0ull : (1ull << box) - 1ull;
-                    keys = 0;
-                    for (int x = 0; x < boxes; ++x)
-                        if (loads >> x & 1) keys |= one << (x << box_log2);
+                if (kLead) {
+                    unsigned long long keys = ~0ull;
+                    if (loads != (1u << boxes) - 1u) {
+                        const unsigned long long one = box == 64 ? ~0ull : (1ull << box) - 1ull;
+                        keys = 0;
+                        for (int x = 0; x < boxes; ++x)
+                            if (loads >> x & 1) keys |= one << (x << box_log2);
+                    }
+                    if (p.len - k0 < kTileKeys) keys &= p.len > k0 ? (1ull << (p.len - k0)) - 1ull : 0ull;
+                    Stage& st = ring.stage[s];
+                    if (t == p.t0) st = d;
+                    st.present = keys;
+                    st.flags = (t == p.t0 ? d.flags : 0) | (t == p.t1 - 1 ? kLast : 0);
                 }
-                if (p.len - k0 < kTileKeys) keys &= p.len > k0 ? (1ull << (p.len - k0)) - 1ull : 0ull;
-                Stage& st = ring.stage[s];
-                if (t == p.t0) st = d;
-                st.present = keys;
-                st.flags = (t == p.t0 ? d.flags : 0) | (t == p.t1 - 1 ? kLast : 0);
-                mbar_arrive_expect_tx(&ring.full[s], __popc(loads) * box * (C::kKPanels + C::kVPanels) * 128);
+                mbar_arrive_expect_tx(&ring.full[s], __popc(loads) * box * (kK + kV) * 128);
             }
             __syncwarp();
             if (load) {
                 uint8_t* dst = smem + s * C::kStageBytes + (lane << box_log2) * 128;
                 const int z = entry * a.g.Hkv + hk, y = key & (page - 1);
 #pragma unroll
-                for (int x = 0; x < C::kKPanels; ++x)
+                for (int x = 0; x < kK; ++x)
                     tma_load_3d(dst + x * kPanelBytes, tmK, &ring.full[s], C::kPanelCols * x, y, z);
 #pragma unroll
-                for (int x = 0; x < C::kVPanels; ++x)
+                for (int x = 0; x < kV; ++x)
                     tma_load_3d(dst + C::kKBytes + x * kPanelBytes, tmV, &ring.full[s], C::kPanelCols * x, y, z);
             }
             if (++s == kStages) {
@@ -190,7 +201,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
     }
     const bool stopped = going && ring_wait(ring, &ring.empty[s], parity, budget_ns);
     if (stopped && lane == 0) {
-        ring.stage[s].flags = kStop;
+        if (kLead) ring.stage[s].flags = kStop;
         mbar_arrive(&ring.full[s]);
     }
     // No copy may be in flight into shared memory that the CTA gives back. (The

@@ -16,11 +16,18 @@
 // through ldmatrix without bank conflicts. Query rows past 16 go to further
 // groups of four warps that read the same tiles.
 //
-// mma.sync and not tcgen05: 16 query rows are an eighth of a tcgen05 tile, its
-// accumulator would pass through TMEM twice per 64 keys for the softmax, and
-// the four key warps would have to meet at every tile. At 16 rows the tensor
-// work of a tile is a few hundred cycles of an SM that gets 22 bytes a cycle
-// from HBM (a 32 KB tile every 1,450 cycles).
+// mma.sync and not tcgen05, up to 32 rows: 16 query rows are an eighth of a
+// tcgen05 tile, its accumulator would pass through TMEM twice per 64 keys for the
+// softmax, and the four key warps would have to meet at every tile. At 16 rows
+// the tensor work of a tile is a few hundred cycles of an SM that gets 22 bytes a
+// cycle from HBM (a 32 KB tile every 1,450 cycles). At 32 the instruction itself
+// becomes the limit: a tile takes 64 of them a sub-partition, at about 16 cycles.
+//
+// One B200: 4 x 65536 tokens of 8 key heads, d = 128, 4 rows: 6.5 TB/s in pages
+// of 16, 6.0 in pages of 8; 4 x 65536 to 262144 in pages of 64: 6.7 TB/s (the
+// measured copy runs at 6.54). 64 sequences of 128 to 16384: 6.1 TB/s. The rest
+// of a small call is latency: 1.7 us until the first copy is issued, 0.8 for it to
+// arrive, about 1 us a tile and 1 us to join.
 #pragma once
 
 #include <type_traits>
@@ -38,7 +45,8 @@ struct DecodeCfg {
     static constexpr int kPanelCols = 64, kKPanels = DK / 64, kVPanels = DV / 64;
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
-    static constexpr int kThreads = (kKeyWarps * R + 1) * 32;
+    static constexpr int kProducers = R == 2 ? 2 : 1;
+    static constexpr int kThreads = (kKeyWarps * R + kProducers) * 32;
     // Outputs of a group's four warps, when a piece ends: with one group in the
     // stage of the piece's last tile, if they fit, else beside the stages.
     static constexpr int kScratchBytes = kKeyWarps * 16 * DV * 4;
@@ -106,9 +114,9 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     __shared__ float2 team_ml[kTeamed ? 16 : 1];          // maximum and sum of each row, for the team
 
     std::conditional_t<kTeamed, Member, Walker> w;
-    if (kTeamed || warp == kKeyWarps * R) w.start(a);     // while the barriers are set up
+    if (kTeamed || warp >= kKeyWarps * R) w.start(a);     // while the barriers are set up
     if (kTeamed && threadIdx.x < 16) team_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
-    const bool going = set_up<kTeamed>(parts, ring, smem, kKeyWarps * R);
+    const bool going = set_up<kTeamed>(parts, ring, smem, kKeyWarps * R, C::kProducers);
     if (!kTeamed && !going) return;
 
     auto consume = [&] {
@@ -389,10 +397,16 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     }
     };
 
-    if (warp == kKeyWarps * R) {
-        if (going)
-            produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns,
-                   [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); });
+    if (warp >= kKeyWarps * R) {
+        auto begin = [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); };
+        if (!going) {
+        } else if (C::kProducers == 1) {
+            produce<C, Loads::kBoth>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
+        } else if (warp == kKeyWarps * R) {
+            produce<C, Loads::kKeys>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
+        } else {
+            produce<C, Loads::kValues>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
+        }
     } else if (going) {
         consume();
     }

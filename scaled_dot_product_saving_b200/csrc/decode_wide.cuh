@@ -34,7 +34,7 @@ struct DecodeWideCfg {
     // leaves 3 KB for what is declared in the kernel).
     static constexpr int kFit = (224 * 1024 - 2 * kQBytes) / kStageBytes, kStages = kFit < 7 ? kFit : 7;
     static constexpr int kOffQ = kStages * kStageBytes, kSmemBytes = kOffQ + 2 * kQBytes;
-    static constexpr int kThreads = 11 * 32;               // two softmax warpgroups, producer, two MMA issuers
+    static constexpr int kThreads = 12 * 32;               // two softmax warpgroups, two MMA issuers, two producers
     static constexpr uint32_t kColS = 0, kColO = 4 * kTileKeys;      // S at 64 (tile % 4), O_x at 256 + DV x
 };
 
@@ -69,7 +69,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     Walker w;
-    if (warp == 8) w.start(a);
+    if (warp == 8 || warp == 11) w.start(a);
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bars.q_full[x], 1);
@@ -87,7 +87,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         mbar_init(&bars.met, 8);
         mbar_init(&bars.o_free, 8);
     }
-    if (!set_up<false>(parts, ring, smem, 1)) return;      // fences the barriers' initialisation
+    if (!set_up<false>(parts, ring, smem, 1, 2)) return;      // fences the barriers' initialisation
     if (warp == 9) {
         tmem_alloc(&bars.tmem, 512);
         tmem_relinquish();
@@ -98,7 +98,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     const uint32_t tmem = bars.tmem;
 
     if (warp == 8) {
-        // -------------------------------------------------------- producer
+        // ------------------------------------- producer of Q and K, which leads
         if (lane == 0) prefetch_tensor_map(&tmQ);
         int pieces = 0;
         // Piece p's description takes the place of piece p - 4's. Its query rows
@@ -114,7 +114,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         auto q_free = [&] {
             return pieces < 2 || ring_wait(ring, &bars.q_free[pieces & 1], ((pieces >> 1) - 1) & 1, budget_ns);
         };
-        produce<C>(&tmK, &tmV, a, w, ring, smem, budget_ns, [&](const Stage& d) {
+        produce<C, Loads::kKeys>(&tmK, &tmV, a, w, ring, smem, budget_ns, [&](const Stage& d) {
             if (!q_free()) return false;
             if (lane == 0) {
                 const int x = pieces & 1;
@@ -134,6 +134,8 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         }
         for (int p = max(0, pieces - 2); p < pieces; ++p)
             (void)mbar_wait_timed(&bars.q_full[p & 1], (p >> 1) & 1, budget_ns);
+    } else if (warp == 11) {
+        produce<C, Loads::kValues>(&tmK, &tmV, a, w, ring, smem, budget_ns, [](const Stage&) { return true; });
     } else if (warp == 9) {
         // ------------------------------------------------ issuer of S = Q K^T
         const uint32_t leader = elect_leader();

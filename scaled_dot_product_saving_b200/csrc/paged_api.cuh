@@ -6,12 +6,10 @@
 namespace {
 
 namespace pg = attn::paged;
-#ifndef WIDE
-#define WIDE 32
-#endif
 
 // Most CTAs of a decode call, and most CTAs times query rows of an item: what the
 // workspace has slots for (one CTA an SM for items of 128 rows, up to three for 16).
+constexpr int kMmaRows = 32;            // bf16 on mma.sync up to here (see decode_rows)
 constexpr int kDecodeCtas = 3 * 148, kDecodeRows = 48 * 148, kDecodeWideRows = pg::kWideRows * 148;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -87,7 +85,7 @@ struct DecodeWorkspace {
 };
 DecodeWorkspace carve_decode(int dv, long long rows_per_head) {
     DecodeWorkspace w;
-    const size_t rows = 2ull * (rows_per_head > WIDE ? kDecodeWideRows : kDecodeRows);
+    const size_t rows = 2ull * (rows_per_head > kMmaRows ? kDecodeWideRows : kDecodeRows);
     w.o_off = 0;
     w.ml_off = round_up(rows * dv * sizeof(float), 256);
     w.head_off = w.ml_off + round_up(rows * 2 * sizeof(float), 256);
@@ -220,8 +218,10 @@ attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const
                                    parts, grid, 0, st);
 }
 
-// Query rows of an item: as many of a key head's as there are, up to 32 (bf16)
-// or 16 (fp32), since every item reads its keys again.
+// Query rows of an item: as many of a key head's as there are, up to 128 (bf16,
+// tcgen05 above 32) or 16 (fp32), since every item reads its keys again. At 32 rows
+// of 32768 tokens, d = 128, tcgen05 takes 178 us and mma.sync 195, at d = 64 241 and
+// 234; 64 sequences of 100 to 3000 tokens with 24 rows, d = 64, 64 and 52.
 template <int DK, int DV>
 attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                           const pg::Parts& parts, int* grid, bool f32, cudaStream_t st) {
@@ -231,7 +231,7 @@ attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, cons
         return decode_f32<DK, DV, 8, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
     }
     if (a.rows <= 16) return decode_tc<DK, DV, 1>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
-    if (a.rows <= WIDE) return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
+    if (a.rows <= kMmaRows) return decode_tc<DK, DV, 2>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
     return decode_wide<DK, DV>(a, Q, Kp, Vp, O, LSE, parts, grid, st);
 }
 
