@@ -335,8 +335,9 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  * Conventions beyond those of the other calls:
  *  - page is a power of two, 8 to 256; d, dv <= 128 (ATTN_ERR_UNSUPPORTED
  *    beyond) with rows of whole 16 bytes (multiples of 8 in bf16, of 4 in
- *    fp32; ATTN_ERR_SHAPE otherwise). num_pages * Hkv, B * max_pages and
- *    max_pages * page are below 2^31.
+ *    fp32; ATTN_ERR_SHAPE otherwise). num_pages * Hkv and B * max_pages are
+ *    below 2^31, num_pages, max_pages * page and (attn_decode) B * H * n at
+ *    most 2^30.
  *  - Nothing is read back to the host: every call can be captured in a graph
  *    and replayed. What a call finds on the device is checked there. Lengths
  *    are clamped to [0, max_pages * page]. A page number outside

@@ -170,6 +170,8 @@ struct Walker {
         const int items = a.g.Hkv * a.row_tiles;
         while (left > 0) {
             for (;; ++b, off = 0) {
+                // (Past the last sequence only if the lengths change meanwhile.)
+                if (b >= a.g.B) return false;
                 p->nq = queries_of(a, b);
                 if (p->nq <= 0) continue;
                 p->len = clamp_len(__ldg(a.lens + b), a.g);

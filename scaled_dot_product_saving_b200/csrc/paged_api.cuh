@@ -50,8 +50,9 @@ attn_status_t check_cache(int B, int Hkv, int d, int dv, int num_pages, int page
     if (d > pg::kMaxWidth || dv > pg::kMaxWidth) return ATTN_ERR_UNSUPPORTED;
     const int es = dtype == ATTN_F32 ? 4 : 2;
     if (d * es % 16 || dv * es % 16) return ATTN_ERR_SHAPE;
-    if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) ||
-        static_cast<long long>(B) * max_pages >= (1ll << 31) || max_pages > (0x7fffffff >> log2))
+    // Kernels number pages, tokens and what lies a tile or a block past them in 32 bits.
+    if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || num_pages > (1 << 30) ||
+        static_cast<long long>(B) * max_pages >= (1ll << 31) || max_pages > ((1 << 30) >> log2))
         return ATTN_ERR_SHAPE;
     *g = pg::Geometry{B, max_pages, num_pages, Hkv, log2};
     return ATTN_OK;
@@ -96,7 +97,7 @@ DecodeWorkspace carve_decode(int dv, long long rows_per_head) {
 attn_status_t check_decode(int B, int H, int Hkv, int n, int d, int dv, attn_dtype_t dtype) {
     if (dtype != ATTN_F32 && dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
     if (B < 1 || H < 1 || Hkv < 1 || n < 1 || d < 1 || dv < 1 || H % Hkv) return ATTN_ERR_SHAPE;
-    if (static_cast<double>(B) * H * n >= 2147483648.0) return ATTN_ERR_SHAPE;
+    if (static_cast<double>(B) * H * n > 1073741824.0) return ATTN_ERR_SHAPE;
     if (d > pg::kMaxWidth || dv > pg::kMaxWidth) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }

@@ -347,3 +347,61 @@ def test_refusals():
     with pytest.raises(lib.AttnError) as e:
         lib.attn_cache_append(k, k, *(p[:, :, :4].contiguous() for p in pools), *books)
     assert e.value.code == 4
+
+
+@both
+def test_a_pool_of_very_many_pages(in_place):
+    """More pages than the books hold in registers, most of them the caller's."""
+    rng = np.random.default_rng(12)
+    P, B = 300001, 3
+    c = numpy_cache(rng, B, 1, 8, 8, 8, (9, 800, 0), spare=P - 102, M=600, unit=True)
+    assert c["ref"].shape[0] == P
+    c["ref"][rng.random(P) < 0.99] |= 1
+    dev, host = on_gpu(c, "bf16")
+    k, v = rows(rng, B, 1, 3000, 8, "bf16"), rows(rng, B, 1, 3000, 8, "bf16")
+    out = append(dev, host, k, v, (3000, 17, 2900), in_place)
+    assert out[0] == 0 and out[2] > 700
+    assert fork(dev, host, (2, 1, 1), (2000, 500, 813), in_place)[0] == 0
+    assert compact(dev, host, in_place)[2] > 1000
+
+
+def test_captured_round():
+    """A step of a search captured whole, in place: new tokens, attention, new
+    parents, then the pool closed up; replayed while the cache grows."""
+    rng = np.random.default_rng(13)
+    B, Hkv, d, page, M = 4, 2, 64, 8, 6
+    dev, host = on_gpu(numpy_cache(rng, B, Hkv, page, d, d, (3, 9, 0, 16), spare=20, M=M), "bf16")
+    P = host["ref"].shape[0]
+    k, q = rows(rng, B, Hkv, 3, d, "bf16"), rows(rng, B, 4, 3, d, "bf16")
+    src, new_len = ints((1, 1, 0, 3)), ints((3, 0, 1, 2))
+    books = {f"{n}_out": dev[n] for n in BOOKS}
+    ws = torch.empty(lib.attn_cache_workspace_size(B, M, P), dtype=torch.uint8, device="cuda")
+    infos = torch.full((3, 3), -1, dtype=torch.int32, device="cuda")
+    args = (dev["k_pages"], dev["v_pages"], *(dev[n] for n in BOOKS))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.attn_cache_append(k, k, *args, new_len=new_len, info=infos[0], workspace=ws, **books)
+        o, lse = lib.attn_decode(q, *args[:4], q_len=new_len)
+        lib.attn_cache_fork(*args, src, info=infos[1], workspace=ws, **books)
+        lib.attn_cache_compact(*args, info=infos[2], workspace=ws, table_out=dev["table"], ref_out=dev["ref"])
+    for turn in range(6):
+        parents = rng.integers(-1, B, size=B) if turn else np.arange(B)
+        grow = rng.integers(0, 4, size=B)
+        src.copy_(ints(parents))
+        new_len.copy_(ints(grow))
+        k.copy_(rows(rng, B, Hkv, 3, d, "bf16"))
+        g.replay()
+        torch.cuda.synchronize()
+        kk = k.double().cpu().numpy()
+        want = []
+        out = paged.append(kk, kk, *(host[n] for n in POOLS + BOOKS), grow)
+        want.append(out[5])
+        out = paged.fork(*out[:5], parents)
+        want.append(out[5])
+        lens = out[3]
+        out = paged.compact(*out[:5])
+        want.append(out[5])
+        host.update(zip(POOLS + ("table", "ref"), out[:4]), lens=lens)
+        same(dev, {n: host[n] for n in POOLS + BOOKS})
+        assert infos.tolist() == [list(x) for x in want]
+    assert lib.attn_get_device_error() == 0

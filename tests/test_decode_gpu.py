@@ -409,3 +409,32 @@ def test_long_drafts():
     dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, lens), "bf16")
     q = torch.tensor(rng.standard_normal((2, 4, n, 64)), device="cuda").to(torch.bfloat16)
     compare(*run(dev, q), "bf16", host, q)
+
+
+@pytest.mark.parametrize("dt,H", [("bf16", 40), ("bf16", 150), ("f32", 20)])
+def test_many_rows_captured_and_at_once(dt, H):
+    """Many query rows per key head: a call replayed on new queries, and calls at
+    once on two streams, give what calls by themselves give."""
+    rng = np.random.default_rng(20)
+    lens = (1500, 70, 333)
+    dev, host = on_gpu(numpy_cache(rng, 3, 2, 16, 64, 64, lens), dt)
+    qs = [torch.tensor(rng.standard_normal((3, 2 * H, 1, 64)), device="cuda").to(DT[dt]) for _ in range(2)]
+    want = [run(dev, q) for q in qs]
+    compare(*want[0], dt, host, qs[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"], stream=s)
+           for _ in range(3) for q, s in zip(qs, streams)]
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+    q = qs[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, l = lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"])
+    for i in (1, 0):
+        q.copy_(qs[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+    assert lib.attn_get_device_error() == 0

@@ -91,6 +91,21 @@ def test_sizes(L, f):
 
 
 @pytest.mark.parametrize("f", ALL)
+def test_limits_leave_room_for_a_tile(L, f):
+    """Tokens, pages and query rows are numbered in 32 bits, and so is what lies
+    a tile past the last of them."""
+    assert f(L, Hkv=1, H=8, P=(1 << 30) + 1) == 2 if f is decode else f(L, Hkv=1, P=(1 << 30) + 1) == 2
+    for page in (8, 16, 256):
+        assert f(L, B=1, page=page, M=(1 << 30) // page + 1) == 2
+        assert f(L, B=1, page=page, M=(1 << 31) // page - 1) == 2
+        if not torch.cuda.is_available():
+            assert f(L, B=1, page=page, M=(1 << 30) // page) == OK_ON_CPU
+    if f is decode:
+        assert f(L, B=1, H=1, Hkv=1, n=(1 << 30) + 1) == 2
+        assert f(L, B=(1 << 30) + 1, H=1, Hkv=1, M=1) == 2
+
+
+@pytest.mark.parametrize("f", ALL)
 def test_workspace(L, f):
     need = (L.attn_decode_workspace_size(2, 8, 2, 1, 64, 64, 1) if f is decode
             else L.attn_cache_workspace_size(2, 8, 32))
@@ -160,6 +175,13 @@ def test_workspace_sizes(L):
     # bounded: pieces per CTA, whatever the batch and the lengths
     assert (L.attn_decode_workspace_size(512, 64, 8, 4, 128, 128, 1)
             == L.attn_decode_workspace_size(1, 64, 8, 4, 128, 128, 1) < 16 << 20)
+
+
+def test_workspace_of_many_rows(L):
+    """More than 32 rows per key head go through items of 128."""
+    few, many = (L.attn_decode_workspace_size(4, H, 1, 1, 64, 128, 1) for H in (32, 33))
+    assert few < many == L.attn_decode_workspace_size(4, 5000, 1, 1, 64, 128, 1) < 40 << 20
+    assert decode(L, H=66, wsb=L.attn_decode_workspace_size(2, 66, 2, 1, 64, 64, 1) - 1) == 6
 
 
 def test_binding_refuses_before_the_library(L):
