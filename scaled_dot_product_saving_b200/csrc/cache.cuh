@@ -140,6 +140,7 @@ struct Rows {
     const uint4* V;
     uint4* Kp;
     uint4* Vp;
+    const int* new_len;  // append: may be null
     int n;
     int wk, wv, k_rows, v_rows;              // widths, rows of a span
     unsigned k_spans;                        // of a part's K; the rest are of its V
@@ -168,6 +169,11 @@ struct Rows {
         return of(Kp, Vp, wk, wv, flat ? 1ll * B * heads * n : n, heads, n, flat);
     }
 };
+
+// Rows of sequence b that are not padding.
+__device__ __forceinline__ int new_rows(const Rows& r, int b) {
+    return r.new_len ? min(max(__ldg(r.new_len + b), 0), r.n) : r.n;
+}
 
 // Span x of the new rows, all of them one part, to their pages. `wait` is called
 // once the rows are on their way, if `early`, and says whether to go on.
@@ -225,9 +231,13 @@ struct Lanes {
     }
 };
 
-// Span x of the new rows, a part for each head of a sequence.
-__device__ __forceinline__ void append_span(const Books& k, const Rows& r, unsigned x, const Lanes& in_k,
-                                            const Lanes& in_v) {
+// Span x of the new rows, a part for each head of a sequence. Padding is told by
+// the call's own numbers, so that it is passed over, and the first rows are on
+// their way, before the books are there; `ready` waits for them and says whether
+// to go on.
+template <typename F>
+__device__ __forceinline__ bool append_span(const Books& k, const Rows& r, unsigned x, const Lanes& in_k,
+                                            const Lanes& in_v, F&& ready) {
     const Geometry& g = k.g;
     const int page = 1 << g.page_log2;
     const unsigned bh = r.spans.divide(x), b = r.by_heads.divide(bh), h = bh - b * r.by_heads.d;
@@ -235,20 +245,22 @@ __device__ __forceinline__ void append_span(const Books& k, const Rows& r, unsig
     const bool is_v = span >= r.k_spans;
     if (is_v) span -= r.k_spans;
     const int w = is_v ? r.wv : r.wk, i0 = int(span) * (is_v ? r.v_rows : r.k_rows);
-    // Rows that turn out to be padding are not worth reading.
-    const int t0 = __ldcg(k.start + b) + i0, left = __ldcg(k.after + b) - t0;
-    if (left <= 0) return;
+    const int left = new_rows(r, b) - i0;
+    if (left <= 0) return true;
     const uint4* from = (is_v ? r.V : r.K) + (size_t(bh) * r.n + i0) * w + (threadIdx.x & 31);
     uint4* pool = (is_v ? r.Vp : r.Kp);
-    const int* row = k.table_out + size_t(b) * g.M;
     uint4 v[kUnits];
     int p[kUnits];
 #pragma unroll
+    for (int e = 0; e < kUnits; ++e)
+        if ((is_v ? in_v.row[e] : in_k.row[e]) < left) v[e] = __ldcs(from + 32 * e);
+    if (!ready()) return false;
+    const int t0 = __ldcg(k.start + b) + i0;
+    const int* row = k.table_out + size_t(b) * g.M;
+#pragma unroll
     for (int e = 0; e < kUnits; ++e) {
         const int i = is_v ? in_v.row[e] : in_k.row[e];
-        if (i >= left) continue;
-        v[e] = __ldcs(from + 32 * e);
-        p[e] = __ldcg(row + ((t0 + i) >> g.page_log2));
+        if (i < left) p[e] = __ldcg(row + ((t0 + i) >> g.page_log2));
     }
 #pragma unroll
     for (int e = 0; e < kUnits; ++e) {
@@ -256,6 +268,7 @@ __device__ __forceinline__ void append_span(const Books& k, const Rows& r, unsig
         if (i < left && page_ok(p[e], g.P))
             pool[((size_t(p[e]) * g.Hkv + h) * page + ((t0 + i) & (page - 1))) * w + c] = v[e];
     }
+    return true;
 }
 
 // Span x of the moves: rows [0, rows) of every head of the listed pages.
@@ -293,10 +306,18 @@ __global__ void __launch_bounds__(kCopyThreads) append_rows(Books k, Rows r) {
         for (unsigned x = first; x < r.spans.d; x += stride)
             if (!append_span_flat(k, r, x, x == first, wait)) return;
     } else {
-        if (!wait()) return;
         const Lanes in_k(r.wk, r.k_rows), in_v(r.wv, r.v_rows);
         const unsigned items = r.spans.d * unsigned(k.g.B) * unsigned(k.g.Hkv);
-        for (unsigned x = first; x < items; x += stride) append_span(k, r, x, in_k, in_v);
+        bool waited = false;
+        auto ready = [&] {
+            if (waited) return true;
+            waited = true;
+            return wait();
+        };
+        for (unsigned x = first; x < items; x += stride)
+            if (!append_span(k, r, x, in_k, in_v, ready)) return;
+        // The grid ends after the books even if there is nothing but padding.
+        if (blockIdx.x == 0) (void)ready();
     }
 }
 
@@ -316,14 +337,14 @@ __device__ __forceinline__ void move_here(const Books& k, const Rows& r) {
 }
 
 // ------------------------------------------------------------------- append
-__global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const int* new_len, Rows r) {
+__global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, Rows r) {
     grid_launch_dependents();                       // the copy kernel may set up meanwhile
     __shared__ long long scratch[33];
     __shared__ int full_s, shared_s;
     const Geometry& g = k.g;
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = int(cluster_rank());
-    const int page_mask = (1 << g.page_log2) - 1, room = g.M << g.page_log2, n = r.n;
+    const int page_mask = (1 << g.page_log2) - 1, room = g.M << g.page_log2;
     const bool same_ref = k.ref_out == k.ref, same_table = k.table_out == k.table;
     if (tid == 0) full_s = shared_s = 0;
 
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const i
         thread_share(g.B, &b0, &b1);
         for (int b = b0; b < b1; ++b) {
             len = clamp_len(k.lens[b], g);
-            add = new_len ? min(max(new_len[b], 0), n) : n;
+            add = new_rows(r, b);
             if (add > room - len) {
                 full = 1;
                 add = 0;                            // the call is refused as a whole below
@@ -379,7 +400,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, const i
         for (int b = b0; __any_sync(0xffffffffu, b < b1); ++b) {
             if (b < b1 && b1 - b0 > 1) {            // else it is in registers still
                 len = clamp_len(k.lens[b], g);
-                add = new_len ? min(max(new_len[b], 0), n) : n;
+                add = new_rows(r, b);
                 if (add > room - len) add = 0;
             }
             int mine = 0, at = 0;

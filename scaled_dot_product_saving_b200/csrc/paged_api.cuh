@@ -407,9 +407,10 @@ attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, voi
     pg::Rows r = pg::Rows::of_new(K_pages, V_pages, d * es / 16, dv * es / 16, B, Hkv, n);
     r.K = static_cast<const uint4*>(K);
     r.V = static_cast<const uint4*>(V);
+    r.new_len = new_len;
     const unsigned long long spans = r.flat ? r.spans.d : 1ull * r.spans.d * B * Hkv;
     return books_and_rows(pg::append_books, pg::append_rows, k, r, spans, st, [&](auto kern, const pg::Rows& x) {
-        return launch_books(kern, st, k, new_len, x);
+        return launch_books(kern, st, k, x);
     });
 }
 
