@@ -208,26 +208,30 @@ decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts part
             return (2 * size_t(first + c) + (c == 0 ? 1 : 0)) * a.tile_rows + r;
         };
         const float2* ml = reinterpret_cast<const float2*>(parts.ml);
-        for (int c = lane; c < pieces; c += 32) m = fmaxf(m, __ldcg(&ml[row_of(c)].x));
+        // Pieces c + e * split of the 32 from c0 on.
+        float4 o[8];
+        auto outputs = [&](int c0, int c, int end) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + e * split < end && 4 * lane < a.dv)
+                    o[e] = __ldcg(reinterpret_cast<const float4*>(parts.o + row_of(c0 + c + e * split) * a.dv + 4 * lane));
+            }
+        };
+        // The first 32 maxima and sums and the first eight outputs in one go.
+        const float2 none = make_float2(-INFINITY, 0.f), x0 = lane < pieces ? __ldcg(ml + row_of(lane)) : none;
+        outputs(0, part, min(32, pieces));
+        m = x0.x;
+        for (int c = lane + 32; c < pieces; c += 32) m = fmaxf(m, __ldcg(&ml[row_of(c)].x));
         m = simt::warp_max(m);
         const float ms = m == -INFINITY ? 0.f : m;
         for (int c0 = 0; c0 < pieces; c0 += 32) {
-            float w = 0.f;
-            if (c0 + lane < pieces) {
-                const float2 x = __ldcg(ml + row_of(c0 + lane));
-                w = exp2f(x.x - ms);
-                l = fmaf(x.y, w, l);
-            }
+            const float2 x = c0 == 0 ? x0 : c0 + lane < pieces ? __ldcg(ml + row_of(c0 + lane)) : none;
+            const float w = exp2f(x.x - ms);
+            l = fmaf(x.y, w, l);
             const int end = min(32, pieces - c0);
             for (int c = part; c < end; c += 8 * split) {
-                float4 o[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c + e * split < end && 4 * lane < a.dv)
-                        o[e] = __ldcg(reinterpret_cast<const float4*>(
-                            parts.o + row_of(c0 + c + e * split) * a.dv + 4 * lane));
-                }
+                if (c0 + c != part) outputs(c0, c, end);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float f = __shfl_sync(0xffffffffu, w, (c + e * split) & 31);
