@@ -51,12 +51,15 @@ struct DecodeCfg {
     // stage of the piece's last tile, if they fit, else beside the stages.
     static constexpr int kScratchBytes = kKeyWarps * 16 * DV * 4;
     static constexpr bool kInStage = R == 1 && kScratchBytes <= kStageBytes;
-    // CTAs an SM: one for 32 rows; for 16 rows two of 113 KB, or at d = dv = 64,
-    // where a tile is half the bytes and costs a warp 0.7 of the time, three of
-    // 64 KB (24 sequences x 16 heads of about 1,100 tokens: 25.7 us with two,
-    // 21.6 with three, 22.6 with four).
-    static constexpr int kCtasPerSm = R == 2 ? 1 : DK == 64 && DV == 64 ? 3 : 2;
-    static constexpr int kStages = (R == 2 ? 128 : kCtasPerSm == 3 ? 64 : kInStage ? 96 : 72) * 1024 / kStageBytes;
+    // CTAs an SM: for 16 rows two of 113 KB, or at d = dv = 64, where a tile is
+    // half the bytes and costs a warp 0.7 of the time, three of 64 KB (24 sequences
+    // x 16 heads of about 1,100 tokens: 25.7 us with two, 21.6 with three, 22.6 with
+    // four); for 32 rows one, or two at d = dv = 64 (8 sequences of 16500 tokens, 8
+    // key heads, 24 rows: 86.0 us with one, 73.7 with two; 64 of 100 to 3000: 53.4
+    // and 50.6).
+    static constexpr bool kNarrow = DK == 64 && DV == 64;
+    static constexpr int kCtasPerSm = 3 - R + (kNarrow ? 1 : 0);
+    static constexpr int kStages = (R == 2 ? 128 / kCtasPerSm : kNarrow ? 64 : kInStage ? 96 : 72) * 1024 / kStageBytes;
     // A team's CTA leaves its output here for the others: [16][DV].
     static constexpr int kOffTeam = kStages * kStageBytes + (kInStage ? 0 : R * kScratchBytes);
     static constexpr int kSmemBytes = kOffTeam + (kTeamed ? 16 * DV * 4 : 0);
