@@ -1,7 +1,7 @@
 // decode.cuh -- attention of the newest tokens of every sequence over its
 // paged keys and values: what the kernels share, the joining of split items, and
-// the kernel for bf16 that ATTN_PATH_SIMT asks for (the others are decode_tc.cuh
-// and decode_f32.cuh).
+// the kernel for bf16 that ATTN_PATH_SIMT asks for (the others are decode_tc.cuh,
+// decode_wide.cuh and decode_f32.cuh).
 //
 //   S_rj = scale * q_r . k_j  over the keys j that row r may see,
 //   O_r = sum_j softmax(S_r)_j v_j,  LSE_r = ln sum_j exp(S_rj)

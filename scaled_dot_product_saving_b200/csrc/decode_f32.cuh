@@ -23,7 +23,7 @@ namespace paged {
 // DK, DV: padded widths; RB: query rows of a warp (4 or 8); R: groups of RB rows.
 template <int DK, int DV, int RB, int R>
 struct DecodeF32Cfg {
-    static constexpr int kPanelCols = 32, kKPanels = DK / 32, kVPanels = DV / 32;
+    static constexpr int kPanelCols = 32, kKPanels = DK / 32, kVPanels = DV / 32, kQPitch = 0, kQBytes = 0, kOffQ = 0;
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
     // Two CTAs an SM where their stages fit: with 16 consumers instead of 8 the
@@ -60,9 +60,9 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
     if (!set_up<false>(parts, ring, smem, C::kWarps, C::kProducers)) return;
     if (warp >= C::kWarps) {
         auto begin = [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); };
-        if (C::kProducers == 1) produce<C, Loads::kBoth>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
-        else if (warp == C::kWarps) produce<C, Loads::kKeys>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
-        else produce<C, Loads::kValues>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
+        if (C::kProducers == 1) produce<C, Loads::kBoth>(&tmK, &tmV, a, nullptr, w, ring, smem, budget_ns, begin);
+        else if (warp == C::kWarps) produce<C, Loads::kKeys>(&tmK, &tmV, a, nullptr, w, ring, smem, budget_ns, begin);
+        else produce<C, Loads::kValues>(&tmK, &tmV, a, nullptr, w, ring, smem, budget_ns, begin);
         return;
     }
 

@@ -1,11 +1,12 @@
 // decode_ring.cuh -- the stream of key tiles that the decode kernels consume: a
 // ring of shared-memory stages of 64 keys, filled page by page with the TMA by
-// one warp that runs ahead of the others, across the borders of pieces.
+// one or two warps that run ahead of the others, across the borders of pieces.
 //
 // A stage is panels of 64 rows of 128 bytes (64 bf16 or 32 fp32 columns) in the
-// TMA's 128-byte swizzle: the K panels, then the V panels. The producer alone
-// knows the split of the call; it leaves beside each stage what the consumers
-// need: which keys are there, and with the first tile of a piece the piece.
+// TMA's 128-byte swizzle: the K panels, then the V panels. The producers alone
+// know the split of the call; the leading one leaves beside each stage what the
+// consumers need: which keys are there, and with the first tile of a piece the
+// piece, and where a kernel asks for it the query rows.
 //
 // Every wait is bounded and on an mbarrier. One that runs out sets the abort
 // flag, which ends every other wait, and each warp leaves its loop.
@@ -99,18 +100,20 @@ __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups
 // What a producer warp loads. One warp issues a copy in about 100 cycles, and a
 // tile of small pages takes many (16 of 16 tokens at d = 128): where a CTA has
 // an SM to itself, K and V have a warp each (8 sequences of 17000 tokens, 20
-// query rows, pages of 16: 123 us with one, 107
-// with two; in fp32, 4 rows of 32768 tokens, 191 and 167).
+// query rows, pages of 16: 123 us with one, 107 with two; in fp32, 4 rows of 32768
+// tokens, 191 and 167).
 enum class Loads { kBoth, kKeys, kValues };
 
-// A producer warp; the one of K, or of both, leads. A tile is 64 / box pages (box = min(page, 64) tokens, one
-// lane each); 32 table entries are held across the warp and the next 32 are on
-// the way. C: the kernel's configuration; begin(piece): called by the warp
-// when a piece begins, with its description, false to give up.
+// A producer warp; the one of K, or of both, leads. A tile is 64 / box pages (box
+// = min(page, 64) tokens, one lane each); 32 table entries are held across the
+// warp and the next 32 are on the way, as are those of the next piece while this
+// one's tiles are issued. C: the kernel's configuration; Q: the query rows, which
+// come beside a piece's first tile if it wants them (kQPitch); begin(piece):
+// called by the warp when a piece begins, with its description, false to give up.
 template <typename C, Loads kLoads, typename RingT, typename W, typename F>
 __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMap* tmV, const DecodeArgs& a,
-                                        W& w, RingT& ring, uint8_t* smem, unsigned long long budget_ns,
-                                        F&& begin) {
+                                        const __nv_bfloat16* Q, W& w, RingT& ring, uint8_t* smem,
+                                        unsigned long long budget_ns, F&& begin) {
     constexpr int kStages = C::kStages;
     constexpr bool kLead = kLoads != Loads::kValues;
     constexpr int kK = kLoads != Loads::kValues ? C::kKPanels : 0, kV = kLoads != Loads::kKeys ? C::kVPanels : 0;
@@ -124,8 +127,27 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
     int n = 0, s = 0;                               // tiles issued, stage of the next
     uint32_t parity = 1;                            // of the empty barriers: the first round passes
     bool going = true;
-    Piece p;
-    while (going && w.next(a, &p)) {
+    // A piece, the first entries of its table row, and its number of pages.
+    struct Ahead {
+        Piece p;
+        const int* row;
+        int base, last, held, ahead;
+        bool some;
+    };
+    auto next = [&] {
+        Ahead x;
+        x.some = w.next(a, &x.p);
+        if (!x.some) return x;
+        x.row = a.table + size_t(x.p.b) * a.g.M;
+        x.last = pages_of(x.p.len, page_log2);
+        x.base = (x.p.t0 * kTileKeys) >> page_log2;
+        x.held = x.base + lane < x.last ? x.row[x.base + lane] : -1;
+        x.ahead = x.base + 32 + lane < x.last ? x.row[x.base + 32 + lane] : -1;
+        return x;
+    };
+    Ahead now = next(), then = now;
+    for (; going && now.some; now = then) {
+        const Piece& p = now.p;
         const int hk = a.row_tiles == 1 ? p.item : p.item / a.row_tiles;
         const int r0 = (p.item - hk * a.row_tiles) * a.tile_rows;
         Stage d;
@@ -145,20 +167,16 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
             going = false;
             break;
         }
-        const int* row = a.table + size_t(p.b) * a.g.M;
-        const int last = pages_of(p.len, page_log2);
-        int base = (p.t0 * kTileKeys) >> page_log2;
-        int held = base + lane < last ? row[base + lane] : -1;
-        int ahead = base + 32 + lane < last ? row[base + 32 + lane] : -1;
+        constexpr bool with_q = kLead && C::kQPitch > 0;
         for (int t = p.t0; t < p.t1; ++t, ++n) {
             const int k0 = t * kTileKeys, first = k0 >> page_log2;
-            if (first - base >= 32) {
-                base += 32;
-                held = ahead;
-                ahead = base + 32 + lane < last ? row[base + 32 + lane] : -1;
+            if (first - now.base >= 32) {
+                now.base += 32;
+                now.held = now.ahead;
+                now.ahead = now.base + 32 + lane < now.last ? now.row[now.base + 32 + lane] : -1;
             }
             const int key = k0 + (lane << box_log2);
-            const int entry = __shfl_sync(0xffffffffu, held, (key >> page_log2) - base);
+            const int entry = __shfl_sync(0xffffffffu, now.held, (key >> page_log2) - now.base);
             const bool load = lane < boxes && key < p.len && page_ok(entry, a.g.P);
             const unsigned loads = __ballot_sync(0xffffffffu, load);
             if (!ring_wait(ring, &ring.empty[s], parity, budget_ns)) {
@@ -180,9 +198,20 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                     st.present = keys;
                     st.flags = (t == p.t0 ? d.flags : 0) | (t == p.t1 - 1 ? kLast : 0);
                 }
-                mbar_arrive_expect_tx(&ring.full[s], __popc(loads) * box * (kK + kV) * 128);
+                mbar_arrive_expect_tx(&ring.full[s], __popc(loads) * box * (kK + kV) * 128 +
+                                                         (with_q && t == p.t0 ? d.rows * a.d * 2 : 0));
             }
             __syncwarp();
+            if constexpr (with_q) {
+                // Row r begins 16 r bytes into its place and ends at its start.
+                if (t == p.t0 && lane < d.rows) {
+                    uint8_t* dst = smem + C::kOffQ + s * C::kQBytes + lane * C::kQPitch;
+                    const __nv_bfloat16* src = Q + (size_t(d.row) + lane) * a.d;
+                    const int turn = (lane * 16) & (C::kQPitch - 1), first = min(a.d * 2, C::kQPitch - turn);
+                    bulk_load(dst + turn, src, first, &ring.full[s]);
+                    if (first < a.d * 2) bulk_load(dst, src + first / 2, a.d * 2 - first, &ring.full[s]);
+                }
+            }
             if (load) {
                 uint8_t* dst = smem + s * C::kStageBytes + (lane << box_log2) * 128;
                 const int z = entry * a.g.Hkv + hk, y = key & (page - 1);
@@ -197,6 +226,8 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                 s = 0;
                 parity ^= 1;
             }
+            // Once the stages are on the way, or with the piece's last tile.
+            if (t == min(p.t1, p.t0 + kStages) - 1) then = next();
         }
     }
     const bool stopped = going && ring_wait(ring, &ring.empty[s], parity, budget_ns);

@@ -3,18 +3,26 @@
 //
 // The mathematics is decode.cuh's. What bounds it is memory: every key and
 // value is read once from HBM (512 bytes a token and key head at d = 128) and
-// meets the few query rows of its key head, 16 to 64 here. So the design is a
+// meets the few query rows of its key head, up to 32 here. So the design is a
 // stream: one warp copies tiles of 64 keys with the TMA, page by page, through
 // a ring of stages, as far ahead as shared memory lets it and across the
 // borders of pieces; the other warps only consume.
 //
 // Each of four key warps takes 16 keys of every tile and keeps its own running
 // maximum, sum and output for 16 query rows, so that no warp waits for another
-// inside a piece; the four are joined when the piece ends. A warp's scores
-// leave mma.m16n8k16 in the layout in which their exponentials enter the second
-// product, and its share of K and V comes from the TMA's 128-byte-swizzled rows
-// through ldmatrix without bank conflicts. Query rows past 16 go to further
-// groups of four warps that read the same tiles.
+// inside a piece. A warp's scores leave mma.m16n8k16 in the layout in which their
+// exponentials enter the second product, and its share of K and V comes from the
+// TMA's 128-byte-swizzled rows through ldmatrix without bank conflicts. Query rows
+// past 16 go to a second group of four warps that read the same tiles.
+//
+// At the end of a piece the four are joined. Where there is room for it (d = 128, up
+// to 16 rows) they do not wait for that either: each leaves what it has in the place
+// of its own keys in the last tile's stage, and a warp of its own joins and writes
+// the rows while they go on; the query rows come with a piece's first tile. Else
+// they meet twice, and each writes a quarter of the columns. (Meeting costs 3,000
+// cycles a piece, leaving 500; query rows from global memory 800 to 1,900. 200
+// sequences of 30 to 400 tokens, d = 128: 32 key heads 137 us with meetings, 111
+// without; 8 key heads 45.5 and 37.2; 64 sequences of 128 to 16384: 143.4, 144.5.)
 //
 // mma.sync and not tcgen05, up to 32 rows: 16 query rows are an eighth of a
 // tcgen05 tile, its accumulator would pass through TMEM twice per 64 keys for the
@@ -46,23 +54,38 @@ struct DecodeCfg {
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
     static constexpr int kProducers = R == 2 ? 2 : 1;
-    static constexpr int kThreads = (kKeyWarps * R + kProducers) * 32;
-    // Outputs of a group's four warps, when a piece ends: with one group in the
-    // stage of the piece's last tile, if they fit, else beside the stages.
-    static constexpr int kScratchBytes = kKeyWarps * 16 * DV * 4;
-    static constexpr bool kInStage = R == 1 && kScratchBytes <= kStageBytes;
+    static constexpr bool kNarrow = DK == 64 && DV == 64;
+    // A warp of its own joins the key warps' outputs, [16][DV] each, left in the
+    // place of a warp's 16 keys (2 KB of each panel) in the stage of the piece's last
+    // tile. Not where they do not fit there (dv > d); not with two groups, for which
+    // one warp is too slow (200 x 64 tokens, 20 rows, d = 128: 49.5 us against 41.0),
+    // nor at d = dv = 64, where three CTAs of six warps leave a thread 96 registers (24
+    // drafts: 22.4 against 21.6): there the key warps meet.
+    static constexpr int kWarpRows = 2048 / (DV * 4);                             // rows in 2 KB
+    static constexpr bool kJoiner = R == 1 && !kNarrow && kWarpRows * (kKPanels + kVPanels) >= 16;
+    static constexpr int kThreads = (kKeyWarps * R + kProducers + (kJoiner ? 1 : 0)) * 32;
     // CTAs an SM: for 16 rows two of 113 KB, or at d = dv = 64, where a tile is
-    // half the bytes and costs a warp 0.7 of the time, three of 64 KB (24 sequences
+    // half the bytes and costs a warp 0.7 of the time, three of 72 KB (24 sequences
     // x 16 heads of about 1,100 tokens: 25.7 us with two, 21.6 with three, 22.6 with
     // four); for 32 rows one, or two at d = dv = 64 (8 sequences of 16500 tokens, 8
     // key heads, 24 rows: 86.0 us with one, 73.7 with two; 64 of 100 to 3000: 53.4
     // and 50.6).
-    static constexpr bool kNarrow = DK == 64 && DV == 64;
     static constexpr int kCtasPerSm = 3 - R + (kNarrow ? 1 : 0);
-    static constexpr int kStages = (R == 2 ? 128 / kCtasPerSm : kNarrow ? 64 : kInStage ? 96 : 72) * 1024 / kStageBytes;
-    // A team's CTA leaves its output here for the others: [16][DV].
-    static constexpr int kOffTeam = kStages * kStageBytes + (kInStage ? 0 : R * kScratchBytes);
-    static constexpr int kSmemBytes = kOffTeam + (kTeamed ? 16 * DV * 4 : 0);
+    static constexpr int kStages = R == 2 ? 128 * 1024 / kCtasPerSm / kStageBytes : kNarrow ? 4 : 3;
+    // Where the key warps meet: all their outputs, in the stage of the piece's last
+    // tile, if they fit, or beside the stages.
+    static constexpr int kScratchBytes = kKeyWarps * 16 * DV * 4;
+    static constexpr bool kInStage = R == 1 && kScratchBytes <= kStageBytes;
+    static constexpr int kOffOut = kStages * kStageBytes;
+    // Query rows of a piece that begins in a stage (where there is room), each turned
+    // by 16 bytes more than the one before, so that ldmatrix meets no bank twice.
+    static constexpr int kOffQ = kOffOut + (kInStage || kJoiner ? 0 : R * kScratchBytes);
+    static constexpr int kQPitch = !kNarrow && (kJoiner || R == 2) ? DK * 2 : 0, kQBytes = 16 * R * kQPitch;
+    // A team's CTA leaves its output here for the others, [16][DV]: its only piece
+    // has read its query rows.
+    static constexpr int kOffTeam = kOffQ;
+    static constexpr int kTeamBytes = kTeamed ? 16 * DV * 4 : 0;
+    static constexpr int kSmemBytes = kOffQ + (kStages * kQBytes > kTeamBytes ? kStages * kQBytes : kTeamBytes);
     static_assert(!kTeamed || R == 1, "a team has one group of rows");
 };
 
@@ -90,6 +113,14 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
+// Row r of the output that key warp kg leaves for the joining warp when a piece
+// ends with the tile in stage s; blocks of 8 columns lie at block ^ (r % 8).
+template <typename C>
+__device__ __forceinline__ uint8_t* out_row(uint8_t* smem, int s, int kg, int r) {
+    return smem + s * C::kStageBytes + (r / C::kWarpRows) * kPanelBytes + kg * 2048 +
+           (r % C::kWarpRows) * (2048 / C::kWarpRows);
+}
+
 // An address of this CTA's shared memory in another CTA of the cluster.
 __device__ __forceinline__ uint32_t of_member(uint32_t addr, int rank) {
     uint32_t r;
@@ -110,16 +141,23 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     using C = DecodeCfg<DK, DV, R, kTeamed>;
     constexpr int kTileRows = 16 * R, kStages = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int kKeys = kKeyWarps * R;                  // key warps; then the producers, then the joining warp
     __shared__ Ring<kStages, R> ring;
-    __shared__ float stat_m[R][kKeyWarps][16], stat_l[R][kKeyWarps][16];
+    // Maxima and sums of the key warps; with a joining warp by the stage of a piece's
+    // last tile, and the warps' arrivals there.
+    constexpr int kSlots = C::kJoiner ? kStages : R;
+    __shared__ float2 stat[kSlots][kKeyWarps][16];
+    __shared__ uint64_t left[kSlots];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     __shared__ float2 team_ml[kTeamed ? 16 : 1];          // maximum and sum of each row, for the team
 
     std::conditional_t<kTeamed, Member, Walker> w;
-    if (kTeamed || warp >= kKeyWarps * R) w.start(a);     // while the barriers are set up
+    if (kTeamed || (warp >= kKeys && warp < kKeys + C::kProducers)) w.start(a);   // while the barriers are set up
+    if (threadIdx.x == 0)
+        for (int x = 0; x < kSlots; ++x) mbar_init(&left[x], kKeys);
     if (kTeamed && threadIdx.x < 16) team_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
-    const bool going = set_up<kTeamed>(parts, ring, smem, kKeyWarps * R, C::kProducers);
+    const bool going = set_up<kTeamed>(parts, ring, smem, kKeys + (C::kJoiner ? 1 : 0), C::kProducers);   // fences the barriers' initialisation
     if (!kTeamed && !going) return;
 
     auto consume = [&] {
@@ -142,27 +180,46 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     float acc[DV / 8][4];
     int see0 = 0, see1 = 0, see_all = 0, k0 = 0;
 
-    // The four warps of the group joined, when a piece ends: their maxima and
-    // sums meet in shared memory; each scales its output to the common maximum
-    // and leaves it there, and each sums and writes a quarter of the columns.
-    auto finish = [&](uint8_t* scratch) -> bool {
+    auto sums = [&](int slot) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
         if (t4 == 0) {
-            stat_m[mt][kg][g] = m0;
-            stat_m[mt][kg][g + 8] = m1;
-            stat_l[mt][kg][g] = l0;
-            stat_l[mt][kg][g + 8] = l1;
+            stat[slot][kg][g] = make_float2(m0, l0);
+            stat[slot][kg][g + 8] = make_float2(m1, l1);
         }
+    };
+
+    // What this warp has of a piece, where the joining warp finds it.
+    auto leave = [&](int s) {
+        sums(s);
+        __syncwarp();                                     // the warp has read its keys and values
+        uint8_t* ra = out_row<C>(smem, s, kg, g) + t4 * 8;
+        uint8_t* rb = out_row<C>(smem, s, kg, g + 8) + t4 * 8;
+        if (g < at.rows) {
+#pragma unroll
+            for (int x = 0; x < DV / 8; ++x) *reinterpret_cast<float2*>(ra + ((x ^ g) << 5)) = make_float2(acc[x][0], acc[x][1]);
+        }
+        if (g + 8 < at.rows) {
+#pragma unroll
+            for (int x = 0; x < DV / 8; ++x) *reinterpret_cast<float2*>(rb + ((x ^ g) << 5)) = make_float2(acc[x][2], acc[x][3]);
+        }
+        warp_arrive(&left[s]);
+    };
+
+    // The four warps of the group joined, when a piece ends: their maxima and
+    // sums meet in shared memory; each scales its output to the common maximum
+    // and leaves it there, and each sums and writes a quarter of the columns.
+    auto finish = [&](uint8_t* scratch) -> bool {
+        sums(mt);
         warp_arrive(&ring.joint[mt][0]);
         if (!ring_wait(ring, &ring.joint[mt][0], joints, budget_ns)) return false;
         float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
 #pragma unroll
         for (int x = 0; x < kKeyWarps; ++x) {
-            M0 = fmaxf(M0, stat_m[mt][x][g]);
-            M1 = fmaxf(M1, stat_m[mt][x][g + 8]);
+            M0 = fmaxf(M0, stat[mt][x][g].x);
+            M1 = fmaxf(M1, stat[mt][x][g + 8].x);
         }
         const float Z0 = M0 == -INFINITY ? 0.f : M0, Z1 = M1 == -INFINITY ? 0.f : M1;
         const float f0 = ex2(m0 - Z0), f1 = ex2(m1 - Z1);
@@ -172,8 +229,9 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             out[(kg * (DV / 8) + x) * 32] = make_float4(acc[x][0] * f0, acc[x][1] * f0, acc[x][2] * f1, acc[x][3] * f1);
 #pragma unroll
         for (int x = 0; x < kKeyWarps; ++x) {
-            L0 = fmaf(stat_l[mt][x][g], ex2(stat_m[mt][x][g] - Z0), L0);
-            L1 = fmaf(stat_l[mt][x][g + 8], ex2(stat_m[mt][x][g + 8] - Z1), L1);
+            const float2 u0 = stat[mt][x][g], u1 = stat[mt][x][g + 8];
+            L0 = fmaf(u0.y, ex2(u0.x - Z0), L0);
+            L1 = fmaf(u1.y, ex2(u1.x - Z1), L1);
         }
         warp_arrive(&ring.joint[mt][1]);
         const bool all = !kTeamed && (at.flags & (kStarts | kEnds)) == (kStarts | kEnds);
@@ -239,15 +297,27 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             at = piece_at(ring, s);
             const int len = ring.stage[s].len, r = mt * 16 + g;
             // Query rows g and g + 8 as A fragments, widths past d as zeros.
-            const __nv_bfloat16* q = Q + (size_t(at.row) + r) * a.d + 2 * t4;
+            if constexpr (C::kQPitch > 0) {
+                const int row = mt * 16 + (lane & 15);
+                const uint32_t q = sm + C::kOffQ + s * C::kQBytes + row * C::kQPitch;
 #pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) {
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    ldsm4(q + (((row + 2 * ks + (lane >> 4)) << 4) & (C::kQPitch - 1)), qf[ks]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int c = ks * 16 + (x >> 1) * 8;
-                    qf[ks][x] = r + (x & 1) * 8 < at.rows && c < a.d
-                                    ? *reinterpret_cast<const uint32_t*>(q + (x & 1) * 8 * a.d + c)
-                                    : 0u;
+                    for (int x = 0; x < 4; ++x)
+                        if (r + (x & 1) * 8 >= at.rows || 2 * t4 + ks * 16 + (x >> 1) * 8 >= a.d) qf[ks][x] = 0u;
+                }
+            } else {
+                const __nv_bfloat16* q = Q + (size_t(at.row) + r) * a.d + 2 * t4;
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int c = ks * 16 + (x >> 1) * 8;
+                        qf[ks][x] = r + (x & 1) * 8 < at.rows && c < a.d
+                                        ? *reinterpret_cast<const uint32_t*>(q + (x & 1) * 8 * a.d + c)
+                                        : 0u;
+                    }
                 }
             }
             // Keys that rows g and g + 8 see, and that every row sees.
@@ -391,27 +461,116 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         }
         k0 += kTileKeys;
         if (flags & kLast) {
-            // Every warp of the group has read the stage once they have met.
-            uint8_t* scratch = smem + (C::kInStage ? s * C::kStageBytes : kStages * C::kStageBytes + mt * C::kScratchBytes);
-            if (!finish(scratch)) return;
-            if (C::kInStage) fence_proxy_async_smem();    // before the TMA writes there again
+            if constexpr (C::kJoiner) {
+                leave(s);
+            } else {
+                // Every warp of the group has read the stage once they have met.
+                uint8_t* scratch = smem + (C::kInStage ? s * C::kStageBytes : C::kOffOut + mt * C::kScratchBytes);
+                if (!finish(scratch)) return;
+                if (C::kInStage) fence_proxy_async_smem();    // before the TMA writes there again
+            }
         }
         warp_arrive(&ring.empty[s]);
     }
     };
 
-    if (warp >= kKeyWarps * R) {
-        auto begin = [&](const Stage& p) { return prefetch_rows(Q, p.row, p.rows, a.d); };
-        if (!going) {
-        } else if (C::kProducers == 1) {
-            produce<C, Loads::kBoth>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
-        } else if (warp == kKeyWarps * R) {
-            produce<C, Loads::kKeys>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
-        } else {
-            produce<C, Loads::kValues>(&tmK, &tmV, a, w, ring, smem, budget_ns, begin);
+    // The joining warp follows the stream and takes what the key warps left of each
+    // piece: O = sum_w 2^(m_w - m) o_w, with its maximum and sum, or divided by the sum
+    // if the piece is its whole item. A row is 4 columns a lane.
+    auto join = [&] {
+    At at{};
+    uint32_t parity = 0, turn = 0;                        // turn: parity of left, a bit a stage
+    constexpr int kLanes = DV / 4, kRowsAtOnce = 32 / kLanes;
+    const int col = lane % kLanes, sub = lane / kLanes;
+    for (int s = 0;; s = s + 1 == kStages ? 0 : s + 1, parity ^= s == 0) {
+        if (!ring_wait(ring, &ring.full[s], parity, budget_ns)) return;
+        const int flags = ring.stage[s].flags;
+        if (flags & kStop) return;
+        if (flags & kFirst) at = piece_at(ring, s);
+        if (!(flags & kLast)) {
+            warp_arrive(&ring.empty[s]);
+            continue;
         }
-    } else if (going) {
+        if (!ring_wait(ring, &left[s], (turn >> s) & 1, budget_ns)) return;
+        turn ^= 1u << s;
+        const bool all = !kTeamed && (at.flags & (kStarts | kEnds)) == (kStarts | kEnds);
+        const size_t first = all ? size_t(at.row) : (2 * size_t(blockIdx.x) + (at.flags & kStarts ? 1 : 0)) * kTileRows;
+        if (!kTeamed && !all && lane == 0) note_head(parts, at);
+        const int mine = lane & 15;                     // statistics: a row a lane
+        float2 x[kKeyWarps];
+        float M = -INFINITY, L = 0.f, f[kKeyWarps];
+#pragma unroll
+        for (int k = 0; k < kKeyWarps; ++k) {
+            x[k] = stat[s][k][mine];
+            M = fmaxf(M, x[k].x);
+        }
+        const float Z = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int k = 0; k < kKeyWarps; ++k) {
+            f[k] = ex2(x[k].x - Z);
+            L = fmaf(x[k].y, f[k], L);
+        }
+        const float inv = all ? (L > 0.f ? 1.f / L : L == 0.f ? 0.f : L) : 1.f;          // NaN stays
+        const bool put = mine < at.rows && (!all || query_of(a, at, mine) < at.nq);
+        const unsigned puts = __ballot_sync(0xffffffffu, put);
+        if (lane < 16 && put) {
+            if constexpr (kTeamed) team_ml[mine] = make_float2(M, L);
+            else if (all) LSE[first + mine] = (M + log2f(L)) * kLn2;
+            else *reinterpret_cast<float2*>(parts.ml + (first + mine) * 2) = make_float2(M, L);
+        }
+        // Four rows at once: what bounds this warp is the latency of its reads.
+        constexpr int kBatch = 4 / kRowsAtOnce;
+        for (int r0 = 0; r0 < at.rows; r0 += 4) {
+            float4 o[kBatch][kKeyWarps];
+#pragma unroll
+            for (int y0 = 0; y0 < kBatch; ++y0) {
+                const int r = r0 + y0 * kRowsAtOnce + sub;
+#pragma unroll
+                for (int k = 0; k < kKeyWarps; ++k)
+                    o[y0][k] = *reinterpret_cast<const float4*>(out_row<C>(smem, s, k, r) +
+                                                               (((col >> 1) ^ (r & 7)) << 5) + (col & 1) * 16);
+            }
+#pragma unroll
+            for (int y0 = 0; y0 < kBatch; ++y0) {
+                const int r = r0 + y0 * kRowsAtOnce + sub;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kKeyWarps; ++k) {
+                    const float fk = __shfl_sync(0xffffffffu, f[k], r);
+                    y.x = fmaf(o[y0][k].x, fk, y.x);
+                    y.y = fmaf(o[y0][k].y, fk, y.y);
+                    y.z = fmaf(o[y0][k].z, fk, y.z);
+                    y.w = fmaf(o[y0][k].w, fk, y.w);
+                }
+                const float i = __shfl_sync(0xffffffffu, inv, r);
+                const size_t to = (first + r) * a.dv + 4 * col;
+                if (!(puts >> r & 1)) {
+                } else if (kTeamed) {
+                    *reinterpret_cast<float4*>(smem + C::kOffTeam + (r * DV + 4 * col) * 4) = y;
+                } else if (4 * col < a.dv) {
+                    if (all)
+                        *reinterpret_cast<uint2*>(O + to) =
+                            make_uint2(pack_bf16x2(y.x * i, y.y * i), pack_bf16x2(y.z * i, y.w * i));
+                    else
+                        *reinterpret_cast<float4*>(parts.o + to) = y;
+                }
+            }
+        }
+        fence_proxy_async_smem();                       // before the TMA writes there again
+        warp_arrive(&ring.empty[s]);
+    }
+    };
+
+    if (!going) {
+    } else if (warp < kKeys) {
         consume();
+    } else if (C::kJoiner && warp == kKeys + C::kProducers) {
+        if constexpr (C::kJoiner) join();
+    } else {
+        auto begin = [&](const Stage& p) { return C::kQPitch > 0 || prefetch_rows(Q, p.row, p.rows, a.d); };
+        if (C::kProducers == 1) produce<C, Loads::kBoth>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns, begin);
+        else if (warp == kKeys) produce<C, Loads::kKeys>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns, begin);
+        else produce<C, Loads::kValues>(&tmK, &tmV, a, Q, w, ring, smem, budget_ns, begin);
     }
     if constexpr (kTeamed) {
         // The team joined: every CTA takes an eighth of the columns of all rows

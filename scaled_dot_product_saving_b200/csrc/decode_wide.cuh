@@ -26,7 +26,7 @@ constexpr int kWideRows = 128;
 
 template <int DK, int DV>
 struct DecodeWideCfg {
-    static constexpr int kPanelCols = 64, kKPanels = DK / 64, kVPanels = DV / 64;
+    static constexpr int kPanelCols = 64, kKPanels = DK / 64, kVPanels = DV / 64, kQPitch = 0;
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
     static constexpr int kQPanelBytes = kWideRows * 128, kQBytes = kKPanels * kQPanelBytes;
@@ -114,7 +114,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         auto q_free = [&] {
             return pieces < 2 || ring_wait(ring, &bars.q_free[pieces & 1], ((pieces >> 1) - 1) & 1, budget_ns);
         };
-        produce<C, Loads::kKeys>(&tmK, &tmV, a, w, ring, smem, budget_ns, [&](const Stage& d) {
+        produce<C, Loads::kKeys>(&tmK, &tmV, a, nullptr, w, ring, smem, budget_ns, [&](const Stage& d) {
             if (!q_free()) return false;
             if (lane == 0) {
                 const int x = pieces & 1;
@@ -135,7 +135,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         for (int p = max(0, pieces - 2); p < pieces; ++p)
             (void)mbar_wait_timed(&bars.q_full[p & 1], (p >> 1) & 1, budget_ns);
     } else if (warp == 11) {
-        produce<C, Loads::kValues>(&tmK, &tmV, a, w, ring, smem, budget_ns, [](const Stage&) { return true; });
+        produce<C, Loads::kValues>(&tmK, &tmV, a, nullptr, w, ring, smem, budget_ns, [](const Stage&) { return true; });
     } else if (warp == 9) {
         // ------------------------------------------------ issuer of S = Q K^T
         const uint32_t leader = elect_leader();

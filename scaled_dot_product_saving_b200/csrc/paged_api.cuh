@@ -7,9 +7,9 @@ namespace {
 
 namespace pg = attn::paged;
 
+constexpr int kMmaRows = 32;            // bf16 on mma.sync up to here (see decode_rows)
 // Most CTAs of a decode call, and most CTAs times query rows of an item: what the
 // workspace has slots for (one CTA an SM for items of 128 rows, up to three for 16).
-constexpr int kMmaRows = 32;            // bf16 on mma.sync up to here (see decode_rows)
 constexpr int kDecodeCtas = 3 * 148, kDecodeRows = 48 * 148, kDecodeWideRows = pg::kWideRows * 148;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -220,9 +220,10 @@ attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const
 }
 
 // Query rows of an item: as many of a key head's as there are, up to 128 (bf16,
-// tcgen05 above 32) or 16 (fp32), since every item reads its keys again. At 32 rows
-// of 32768 tokens, d = 128, tcgen05 takes 178 us and mma.sync 195, at d = 64 241 and
-// 234; 64 sequences of 100 to 3000 tokens with 24 rows, d = 64, 64 and 52.
+// tcgen05 above 32) or 16 (fp32), since every item reads its keys again. 8 x 32768
+// tokens, 32 rows: tcgen05 takes 172 us and mma.sync 196 at d = 128, 138 and 133 at d
+// = 64; 64 sequences of 100 to 3000 tokens, 24 rows: 83 and 76, 69 and 50; 200 of 30 to
+// 400, 20 rows, d = 128: 125 and 80. The host does not know the lengths.
 template <int DK, int DV>
 attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                           const pg::Parts& parts, int* grid, bool f32, cudaStream_t st) {

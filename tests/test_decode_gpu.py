@@ -438,3 +438,41 @@ def test_many_rows_captured_and_at_once(dt, H):
         torch.cuda.synchronize()
         assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
     assert lib.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("H,d,dv,page", [(4, 128, 128, 16), (16, 128, 128, 64), (64, 128, 64, 8), (12, 72, 40, 16),
+                                         (40, 128, 128, 32), (8, 64, 64, 16), (8, 48, 128, 16)])
+def test_many_short_sequences(H, d, dv, page):
+    """Several pieces in a row to every CTA, most of a single tile, some of none."""
+    rng = np.random.default_rng(21)
+    B, n = 400, 2
+    lens = rng.integers(0, 150, size=B)
+    lens[[0, 7, 250]] = (700, 0, 640)
+    q_len = rng.integers(0, n + 1, size=B)
+    dev, host = on_gpu(numpy_cache(rng, B, 4, page, d, dv, lens), "bf16")
+    q = torch.tensor(rng.standard_normal((B, H, n, d)), device="cuda").to(torch.bfloat16)
+    out = torch.full((B, H, n, dv), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, H, n), 7.0, device="cuda")
+    run(dev, q, q_len=q_len, out=out, lse=lse)
+    compare(out, lse, "bf16", host, q, q_len=q_len)
+    idle = torch.tensor(np.arange(n)[None, :] >= q_len[:, None], device="cuda")
+    assert (out.transpose(1, 2)[idle] == 7).all() and (lse.transpose(1, 2)[idle] == 7).all()
+    again = run(dev, q, q_len=q_len, out=out.clone(), lse=lse.clone())
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@SPLITS
+def test_a_query_of_nan_among_wide_heads(room):
+    """d = 128: a query row that is not a number leaves the others as they are."""
+    rng = np.random.default_rng(22)
+    lens = (300, 64)
+    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 128, 128, lens, M=width(lens, 16, room)), "bf16")
+    q = torch.tensor(rng.standard_normal((2, 12, 1, 128)), device="cuda").to(torch.bfloat16)
+    want = run(dev, q)
+    q[0, 2], q[1, 11] = float("nan"), float("inf")
+    o, lse = run(dev, q)
+    hit = torch.zeros(2, 12, 1, dtype=torch.bool, device="cuda")
+    hit[0, 2] = hit[1, 11] = True
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    for got, ref, mask in ((o, want[0], ~hit), (lse, want[1], ~hit)):
+        assert torch.equal(got[mask], ref[mask])
