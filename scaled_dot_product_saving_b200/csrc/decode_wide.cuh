@@ -15,6 +15,10 @@
 // its next scores ready when it has left its weights; another issues the second
 // ones. (What bounded the kernel with one issuing warp was that warp: two waits,
 // twelve MMAs and a message to the stream, 1,900 cycles a tile.)
+//
+// One B200, 8 sequences of 32768 tokens, 8 key heads, d = 128: 64 rows 186 us, 128
+// rows 205 (5.8 and 5.2 TB/s). 8 of 16384 to 32768 tokens, 16 key heads, d = 64, 48
+// rows: 228 us (3.4 TB/s); a tile has half the bytes, and the softmax bounds it.
 #pragma once
 
 #include "decode_ring.cuh"
