@@ -369,7 +369,9 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  *          j >= L - (c - 1 - i): query i is token L - c + i
  *   P = softmax(S),  O = P V,  LSE_i = log sum_j exp(S_ij)
  *   Q [B,H,n,d], O [B,H,n,dv] element type; LSE [B,H,n] fp32.
- * A query that sees no key (an empty sequence) gets O = 0 and LSE = -inf. Rows
+ * A query that sees no key (an empty sequence) gets O = 0 and LSE = -inf, and so
+ * does one whose scores are all -inf; a score of -inf weighs nothing. A score of
+ * +inf gives LSE = +inf and O = NaN, one of NaN gives NaN in both. Rows
  * i >= q_len[b] of O and LSE are left as they were. What unused rows of a page
  * hold (NaN included) has no influence. H must be a multiple of Hkv.
  * Pieces of a long sequence are joined in a fixed order: a repeated call gives

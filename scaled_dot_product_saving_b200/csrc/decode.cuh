@@ -25,6 +25,10 @@ namespace paged {
 constexpr int kRows = 16;             // query rows per item on the CUDA cores
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxWidth = 128;
+// Where a running maximum stops (the largest finite number): a score of +inf then
+// weighs 2^inf = inf, not 2^(inf - inf), so that LSE is +inf and O = inf / inf is NaN,
+// as the logarithm of the sum and the softmax have it. A score of NaN makes both NaN.
+constexpr float kTopScore = 3.402823466e38f;
 
 // Last key (exclusive) that query i of nq sees in a sequence of len tokens,
 // the queries being its last nq tokens.
@@ -118,7 +122,7 @@ decode_simt(DecodeArgs a, const __nv_bfloat16* __restrict__ Q, const __nv_bfloat
             for (int r = warp; r < rows; r += kSimtThreads / 32) {
                 const float s0 = Ps[r * kTileKeys + lane], s1 = Ps[r * kTileKeys + 32 + lane];
                 const float old = Ms[r];
-                const float m = fmaxf(old, simt::warp_max(fmaxf(s0, s1)));
+                const float m = fminf(fmaxf(old, simt::warp_max(fmaxf(s0, s1))), kTopScore);
                 const float ms = m == -INFINITY ? 0.f : m;     // a row without keys so far
                 const float e0 = exp2f(s0 - ms), e1 = exp2f(s1 - ms), c = exp2f(old - ms);
                 const float sum = simt::warp_sum(e0 + e1);

@@ -263,7 +263,7 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                     float f[kSets];
 #pragma unroll
                     for (int x = 0; x < kSets; ++x) {
-                        const float next = fmaxf(m[x], top[x]);
+                        const float next = fminf(fmaxf(m[x], top[x]), kTopScore);
                         f[x] = next == -INFINITY ? 1.f : exp2f(m[x] - next);
                         m[x] = next;
                         l[x] *= f[x];

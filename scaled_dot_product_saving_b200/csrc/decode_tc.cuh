@@ -370,7 +370,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 // a maximum has grown by more than 8 (base 2): weights stay below
                 // 2^8 and are summed in fp32.
                 if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
-                    const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+                    const float n0 = fminf(fmaxf(m0, x0), kTopScore), n1 = fminf(fmaxf(m1, x1), kTopScore);
                     const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
                     m0 = n0;
                     m1 = n1;

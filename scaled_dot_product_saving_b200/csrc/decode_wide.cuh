@@ -333,8 +333,9 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                     if (__any_sync(0xffffffffu, want)) {
                         float alpha = 1.f;
                         if (want) {
-                            alpha = ex2(m_run - top);
-                            m_run = top;
+                            const float next = fminf(top, kTopScore);
+                            alpha = ex2(m_run - next);
+                            m_run = next;
                             l_run *= alpha;
                         }
                         if (i >= 2) {

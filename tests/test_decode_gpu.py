@@ -476,3 +476,68 @@ def test_a_query_of_nan_among_wide_heads(room):
     assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
     for got, ref, mask in ((o, want[0], ~hit), (lse, want[1], ~hit)):
         assert torch.equal(got[mask], ref[mask])
+
+
+KERNELS = pytest.mark.parametrize("dt,H,path", [("bf16", 4, "AUTO"), ("bf16", 24, "AUTO"), ("bf16", 40, "AUTO"),
+                                                ("bf16", 12, "SIMT"), ("f32", 4, "AUTO"), ("f32", 8, "AUTO"),
+                                                ("f32", 16, "AUTO")])
+
+
+@SPLITS
+@KERNELS
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_scores(dt, H, path, d, room):
+    """A score of +inf: LSE = +inf and O = softmax = NaN, for its query alone; with
+    a score that is not a number beside it, both NaN. A score of -inf weighs nothing."""
+    rng = np.random.default_rng(24)
+    lens = (1300, 75)
+    c = numpy_cache(rng, 2, 1, 16, d, d, lens, M=width(lens, 16, room))
+    q = rng.standard_normal((2, H, 1, d))
+    q[..., 7] = np.where(np.arange(H) % 3 == 1, 1.0, -1.0)[None, :, None]
+    q = torch.tensor(q, device="cuda").to(DT[dt])
+    up = torch.tensor(np.broadcast_to(np.arange(H)[None, :, None] % 3 == 1, (2, H, 1)).copy(), device="cuda")
+    try:
+        lib.attn_set_path(getattr(lib, f"ATTN_PATH_{path}"))
+        for t in ((0, 0), (65, 64), (700, 70), (1299, 74)):
+            runs = {}
+            for bad in (1e4, np.inf):
+                dirty = {k: v.copy() for k, v in c.items()}
+                for b in range(2):
+                    dirty["k_pages"][c["table"][b, t[b] // 16], 0, t[b] % 16, 7] = bad
+                dev, _ = on_gpu(dirty, dt)
+                runs[bad] = run(dev, q)
+            o, lse = runs[np.inf]
+            assert torch.isposinf(lse[up]).all() and torch.isnan(o[up]).all()
+            # The others: the same weights, perhaps from another running maximum.
+            # In bf16 the weights and the result are rounded once in each call (2^-8 of
+            # sum P |v| <= max |v|); in fp32 errors are some (L + d) 2^-24 of it, below 2^-12.
+            top = float(dev["v_pages"].float().abs().max())
+            far = (o[~up].float() - runs[1e4][0][~up].float()).abs().max()
+            assert far <= (4 * 2.0 ** -8 if dt == "bf16" else 2.0 ** -12) * top
+            assert (lse[~up] - runs[1e4][1][~up]).abs().max() <= 2.0 ** -12 * 16
+            # one more token with a score of NaN
+            for b in range(2):
+                dirty["k_pages"][c["table"][b, 2], 0, 3, 9] = np.nan
+            o, lse = run(on_gpu(dirty, dt)[0], q)
+            assert torch.isnan(lse).all() and torch.isnan(o).all()
+    finally:
+        lib.attn_set_path(lib.ATTN_PATH_AUTO)
+
+
+@SPLITS
+@KERNELS
+def test_scores_of_minus_infinity_alone(dt, H, path, room):
+    """Every score -inf: as if there were no key."""
+    rng = np.random.default_rng(26)
+    lens = (70, 1)
+    c = numpy_cache(rng, 2, 1, 16, 64, 64, lens, M=width(lens, 16, room))
+    c["k_pages"][..., 7] = -np.inf
+    q = rng.standard_normal((2, H, 1, 64))
+    q[..., 7] = 1.0
+    q = torch.tensor(q, device="cuda").to(DT[dt])
+    try:
+        lib.attn_set_path(getattr(lib, f"ATTN_PATH_{path}"))
+        o, lse = run(on_gpu(c, dt)[0], q)
+        assert (o == 0).all() and torch.isneginf(lse).all()
+    finally:
+        lib.attn_set_path(lib.ATTN_PATH_AUTO)
