@@ -373,7 +373,9 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  * does one whose scores are all -inf; a score of -inf weighs nothing. A score of
  * +inf gives LSE = +inf and O = NaN, one of NaN gives NaN in both. Rows
  * i >= q_len[b] of O and LSE are left as they were. What unused rows of a page
- * hold (NaN included) has no influence. H must be a multiple of Hkv.
+ * hold (NaN included) has no influence; an infinite or NaN value of a token makes
+ * its column of O infinite or NaN for every query that sees it, however small the
+ * weight, and for no other. H must be a multiple of Hkv.
  * Pieces of a long sequence are joined in a fixed order: a repeated call gives
  * the same bits. Whole prompts belong to attn_fwd.
  */

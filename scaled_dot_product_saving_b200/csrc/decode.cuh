@@ -141,11 +141,9 @@ decode_simt(DecodeArgs a, const __nv_bfloat16* __restrict__ Q, const __nv_bfloat
                 for (int r = 0; r < kRows; ++r) {
                     if (r < rows) {
                         float s = acc[r] * Cs[r];
-                        for (int j = 0; j < kTileKeys; ++j) {
-                            // A token that this row does not see may hold anything.
-                            const float e = Ps[r * kTileKeys + j];
-                            if (e != 0.f) s = fmaf(e, Vs[j * dv + tid], s);
-                        }
+                        // A token that this row does not see may hold anything.
+                        const int end = min(kTileKeys, visible(a, p.len, p.nq, (r0 + r) % a.n) - k0);
+                        for (int j = 0; j < end; ++j) s = fmaf(Ps[r * kTileKeys + j], Vs[j * dv + tid], s);
                         acc[r] = s;
                     }
                 }

@@ -243,10 +243,14 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 }
                 const int k0 = tile0 + k8;
                 const bool whole = there == 0xffu && k0 + 8 <= see_all;
+                unsigned hidden = 0;                       // rows (a bit a set) that do not see the key
                 if (!whole) {
 #pragma unroll
                     for (int x = 0; x < kSets; ++x)
-                        if (!(there >> my_key & 1) || k0 + my_key >= see[x]) sc[x] = -INFINITY;
+                        if (!(there >> my_key & 1) || k0 + my_key >= see[x]) {
+                            sc[x] = -INFINITY;
+                            hidden |= 1u << x;
+                        }
                 }
                 // Running maximum over the keys of a row (lanes that differ in bits
                 // 2, 3 and 4); the reference moves when it has grown by more than 8.
@@ -281,7 +285,7 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 for (int x = 0; x < kSets; ++x) {
                     const float e = exp2f(sc[x] - (m[x] == -INFINITY ? 0.f : m[x]));
                     l[x] += e;
-                    weights[my_key * RB + 4 * x + my_row] = e;
+                    weights[my_key * RB + 4 * x + my_row] = hidden >> x & 1 ? -0.f : e;
                 }
                 __syncwarp();
 #pragma unroll
@@ -296,8 +300,9 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                         const float e[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            // ... and a token that only some rows see
-                            if (!whole && e[r] == 0.f) continue;
+                            // ... and a token that only some rows see: the others have
+                            // -0 (a weight that vanished is +0, and infinity times it NaN)
+                            if (!whole && __float_as_uint(e[r]) == 0x80000000u) continue;
                             float4& o = acc[4 * x + r];
                             o.x = fmaf(e[r], v.x, o.x);
                             o.y = fmaf(e[r], v.y, o.y);

@@ -432,7 +432,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                     }
                     if (__any_sync(0xffffffffu, odd)) {
                         // Value by value: infinities and NaN times the weights of
-                        // the rows that see them.
+                        // the rows that see them, a weight of zero included.
                         for (int j = 0; j < 16; ++j) {
                             if (!(there >> j & 1)) continue;
                             const int from = (lane & ~3) | ((j & 7) >> 1);
@@ -450,8 +450,8 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                                 for (int x = 0; x < 2; ++x) {
                                     const float y = __uint_as_float(x ? v & 0xffff0000u : v << 16);
                                     if (isfinite(y)) continue;
-                                    if (p0 != 0.f) acc[c][x] += p0 * y;
-                                    if (p1 != 0.f) acc[c][2 + x] += p1 * y;
+                                    if (k0 + j < see0) acc[c][x] += p0 * y;
+                                    if (k0 + j < see1) acc[c][2 + x] += p1 * y;
                                 }
                             }
                         }

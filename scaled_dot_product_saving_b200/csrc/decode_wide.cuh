@@ -423,7 +423,7 @@ decode_wide(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 const float v = c0 + e < a.dv ? __bfloat162float(Vp[row * a.dv + c0 + e]) : 0.f;
-                                if (!isfinite(v) && wgt != 0.f) y[e] += wgt * v;
+                                if (!isfinite(v)) y[e] += wgt * v;
                             }
                         }
                     }

@@ -541,3 +541,37 @@ def test_scores_of_minus_infinity_alone(dt, H, path, room):
         assert (o == 0).all() and torch.isneginf(lse).all()
     finally:
         lib.attn_set_path(lib.ATTN_PATH_AUTO)
+
+
+@SPLITS
+@KERNELS
+@pytest.mark.parametrize("n", [1, 4])
+def test_values_not_finite_of_a_vanishing_weight(dt, H, path, n, room):
+    """A weight that underflows to zero is not a mask: an infinite or NaN value of a
+    token reaches every query that sees it, wherever in a tile the token lies,
+    and no other."""
+    rng = np.random.default_rng(25)
+    lens, heads = (1300, 75), max(1, H // n)
+    c = numpy_cache(rng, 2, 1, 16, 64, 64, lens, M=width(lens, 16, room))
+    q = rng.standard_normal((2, heads, n, 64))
+    q[..., 7] = 8.0
+    q = torch.tensor(q, device="cuda").to(DT[dt])
+    try:
+        lib.attn_set_path(getattr(lib, f"ATTN_PATH_{path}"))
+        for back in (2, 1200, 20):
+            for bad in (np.inf, np.nan):
+                dirty = {k: v.copy() for k, v in c.items()}
+                see = np.zeros((2, heads, n), dtype=bool)
+                for b, L in enumerate(lens):
+                    t = max(L - back, 0)
+                    dirty["k_pages"][c["table"][b, t // 16], 0, t % 16, 7] = -2000.0     # score about -2000
+                    dirty["v_pages"][c["table"][b, t // 16], 0, t % 16, 5] = bad
+                    see[b] = t < L - (n - 1 - np.arange(n))
+                o, lse = run(on_gpu(dirty, dt)[0], q)
+                see = torch.tensor(see, device="cuda")
+                assert torch.isfinite(lse).all()
+                assert not torch.isfinite(o[..., 5][see]).any()
+                assert torch.isfinite(o[..., 5][~see]).all()
+                assert torch.isfinite(o[..., [x for x in range(64) if x != 5]]).all()
+    finally:
+        lib.attn_set_path(lib.ATTN_PATH_AUTO)
