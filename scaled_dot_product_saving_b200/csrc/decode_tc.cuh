@@ -132,6 +132,11 @@ __device__ __forceinline__ float2 ld_member(uint32_t addr) {
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ int ld_member_int(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 
 template <int DK, int DV, int R, bool kTeamed>
 __global__ void __launch_bounds__(DecodeCfg<DK, DV, R, kTeamed>::kThreads, DecodeCfg<DK, DV, R, kTeamed>::kCtasPerSm)
@@ -586,10 +591,12 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             const size_t row = row_base(a, w.p.b, w.p.item / a.row_tiles) + first + r;
             const uint32_t ml = smem_addr(&team_ml[r]), o = smem_addr(smem + C::kOffTeam) + (r * DV + c) * 4;
             float2 x[kTeam], y[kTeam];
+            int gone = 0;                                 // a member gave up: nothing is written
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) {
                 x[k] = ld_member(of_member(ml, k));
                 y[k] = ld_member(of_member(o, k));
+                gone |= ld_member_int(of_member(smem_addr(&ring.abort), k));
             }
             float M = -INFINITY, L = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
@@ -604,7 +611,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 y1 = fmaf(y[k].y, f, y1);
             }
             const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;                // NaN stays
-            if ((first + r) % a.n < w.p.nq) {
+            if (gone == 0 && (first + r) % a.n < w.p.nq) {
                 if (c < a.dv) *reinterpret_cast<uint32_t*>(O + row * a.dv + c) = pack_bf16x2(y0 * inv, y1 * inv);
                 if (c == 0) LSE[row] = (M + log2f(L)) * kLn2;
             }

@@ -575,3 +575,20 @@ def test_values_not_finite_of_a_vanishing_weight(dt, H, path, n, room):
                 assert torch.isfinite(o[..., [x for x in range(64) if x != 5]]).all()
     finally:
         lib.attn_set_path(lib.ATTN_PATH_AUTO)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("room,H", [(None, 4), (5000, 4), (None, 48), (None, 80)])
+def test_after_a_timeout_nothing_is_written(dt, room, H):
+    """While the error word is set the call leaves its outputs as they were,
+    whichever kernel takes it: a team, the split, two row groups, many rows."""
+    rng = np.random.default_rng(23)
+    dev, host = on_gpu(numpy_cache(rng, 2, 2, 16, 64, 64, (90, 30), M=width((90,), 16, room)), dt)
+    q = torch.tensor(rng.standard_normal((2, H, 1, 64)), device="cuda").to(DT[dt])
+    out = torch.full((2, H, 1, 64), 7.0, dtype=DT[dt], device="cuda")
+    lse = torch.full((2, H, 1), 7.0, device="cuda")
+    lib.attn_probe_timeout(1000)
+    lib.attn_decode(q, dev["k_pages"], dev["v_pages"], dev["table"], dev["lens"], out=out, lse=lse)
+    assert lib.attn_get_device_error() == lib.ATTN_ERR_DEVICE_TIMEOUT
+    assert (out == 7).all() and (lse == 7).all()
+    compare(*run(dev, q, out=out, lse=lse), dt, host, q)
