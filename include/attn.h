@@ -348,10 +348,11 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  *    not overlap anything else (ATTN_ERR_ALIAS). Pages are taken lowest
  *    number first, so results do not depend on timing. Pages of the pools
  *    are written in place. `info` [3] int32 in device memory receives
- *      [0] 0: done. 1: not enough free pages. 2: a sequence would outgrow its
- *          table row. 3: (append) a partly filled last page is not the
- *          sequence's alone. In cases 1 to 3 the call changes nothing: the
- *          outputs are copies of the inputs, and no page is written
+ *      [0] 0: done. 1: not enough free pages. 2: (append) a sequence would
+ *          outgrow its table row. 3: (append) a partly filled last page of a
+ *          sequence with new tokens is not that sequence's alone. Of several
+ *          that hold the highest is told. In cases 1 to 3 the call changes
+ *          nothing: the outputs are copies of the inputs, and no page is written
  *      [1] free pages after the call
  *      [2] pages taken (append), copied (fork) or moved (compact)
  *  - A workspace belongs to one call in flight; contents on entry do not

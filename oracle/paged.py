@@ -86,7 +86,7 @@ def append(k, v, k_pages, v_pages, table, lens, ref, new_len=None):
     if any(old[b] + new[b] > M * page for b in range(B)):
         status = INFO_TABLE_FULL
     for b in range(B):
-        if new[b] > 0 and old[b] % page and old[b] + new[b] <= M * page:
+        if new[b] > 0 and old[b] % page:
             p = table[b, old[b] // page]
             if not 0 <= p < P or ref[p] != 1:
                 status = INFO_SHARED_TAIL

@@ -360,14 +360,14 @@ __global__ void __launch_bounds__(kBookThreads, 1) append_books(Books k, Rows r)
         for (int b = b0; b < b1; ++b) {
             len = clamp_len(k.lens[b], g);
             add = new_rows(r, b);
-            if (add > room - len) {
-                full = 1;
-                add = 0;                            // the call is refused as a whole below
-            }
             if (add > 0 && (len & page_mask) != 0) {
                 // The page that goes on being filled must be this sequence's alone.
                 const int p = k.table[size_t(b) * g.M + (len >> g.page_log2)];
                 if (!page_ok(p, g.P) || k.ref[p] != 1) shared = 1;
+            }
+            if (add > room - len) {
+                full = 1;
+                add = 0;                            // the call is refused as a whole below
             }
             need += pages_of(len + add, g.page_log2) - pages_of(len, g.page_log2);
         }

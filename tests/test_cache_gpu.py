@@ -405,3 +405,35 @@ def test_captured_round():
         same(dev, {n: host[n] for n in POOLS + BOOKS})
         assert infos.tolist() == [list(x) for x in want]
     assert lib.attn_get_device_error() == 0
+
+
+@both
+def test_which_refusal_is_told(in_place):
+    """3 goes before 2 and 2 before 1; a partly filled last page is looked at in every
+    sequence with new tokens, whether or not they fit its row."""
+    rng = np.random.default_rng(14)
+    dev, host = on_gpu(numpy_cache(rng, 3, 2, 8, 64, 64, (12, 8, 5), spare=1, M=2), "bf16")
+    k, v = rows(rng, 3, 2, 9, 64, "bf16"), rows(rng, 3, 2, 9, 64, "bf16")
+    host["ref"] = host["ref"].copy()
+
+    def share(b, j, by):
+        p = int(host["table"][b, j])
+        dev["ref"][p] += by
+        host["ref"][p] += by
+
+    assert append(dev, host, k, v, (1, 0, 8), in_place)[0] == 0
+    dev, host = on_gpu(numpy_cache(rng, 3, 2, 8, 64, 64, (12, 8, 5), spare=1, M=2), "bf16")
+    host["ref"] = host["ref"].copy()
+    assert append(dev, host, k, v, (4, 8, 8), in_place)[0] == 1          # one page for two
+    assert append(dev, host, k, v, (5, 8, 8), in_place)[0] == 2          # ... and a full row
+    share(0, 1, 1)
+    assert append(dev, host, k, v, (1, 8, 8), in_place)[0] == 3          # no pages, and a shared last page
+    assert append(dev, host, k, v, (1, 9, 8), in_place)[0] == 3          # a full row elsewhere
+    assert append(dev, host, k, v, (5, 0, 0), in_place)[0] == 3          # the full row is the shared one's
+    assert append(dev, host, k, v, (5, 9, 8), in_place)[0] == 3          # all of them
+    assert append(dev, host, k, v, (0, 9, 1), in_place)[0] == 2          # shared, but not added to
+    share(0, 1, -1)
+    share(2, 0, 1)
+    assert append(dev, host, k, v, (5, 0, 9), in_place)[0] == 3
+    share(2, 0, -1)
+    assert append(dev, host, k, v, (4, 0, 8), in_place)[0] == 0
