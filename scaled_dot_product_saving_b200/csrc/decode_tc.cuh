@@ -50,6 +50,7 @@ constexpr int kKeyWarps = 4;                       // warps that share a tile's 
 // DK, DV: padded widths; R: groups of 16 query rows; kTeamed: a team an item.
 template <int DK, int DV, int R, bool kTeamed>
 struct DecodeCfg {
+    static constexpr int kTileRows = 16 * R;
     static constexpr int kPanelCols = 64, kKPanels = DK / 64, kVPanels = DV / 64;
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;
@@ -68,8 +69,8 @@ struct DecodeCfg {
     // half the bytes and costs a warp 0.7 of the time, three of 72 KB (24 sequences
     // x 16 heads of about 1,100 tokens: 25.7 us with two, 21.6 with three, 22.6 with
     // four); for 32 rows one, or two at d = dv = 64 (8 sequences of 16500 tokens, 8
-    // key heads, 24 rows: 86.0 us with one, 73.7 with two; 64 of 100 to 3000: 53.4
-    // and 50.6).
+    // key heads, 24 rows: 86.0 us with one, 60.0 with two; 64 of 100 to 3000: 53.4
+    // and 44.2).
     static constexpr int kCtasPerSm = 3 - R + (kNarrow ? 1 : 0);
     static constexpr int kStages = R == 2 ? 128 * 1024 / kCtasPerSm / kStageBytes : kNarrow ? 4 : 3;
     // Where the key warps meet: all their outputs, in the stage of the piece's last
@@ -144,7 +145,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
           const __nv_bfloat16* __restrict__ Q, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE,
           Parts parts, unsigned long long budget_ns) {
     using C = DecodeCfg<DK, DV, R, kTeamed>;
-    constexpr int kTileRows = 16 * R, kStages = C::kStages;
+    constexpr int kTileRows = C::kTileRows, kStages = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int kKeys = kKeyWarps * R;                  // key warps; then the producers, then the joining warp
     __shared__ Ring<kStages, R> ring;

@@ -30,6 +30,7 @@ constexpr int kWideRows = 128;
 
 template <int DK, int DV>
 struct DecodeWideCfg {
+    static constexpr int kCtasPerSm = 1, kTileRows = kWideRows;
     static constexpr int kPanelCols = 64, kKPanels = DK / 64, kVPanels = DV / 64, kQPitch = 0;
     static constexpr int kKBytes = kKPanels * kPanelBytes;
     static constexpr int kStageBytes = kKBytes + kVPanels * kPanelBytes;

@@ -9,8 +9,11 @@ namespace pg = attn::paged;
 
 constexpr int kMmaRows = 32;            // bf16 on mma.sync up to here (see decode_rows)
 // Most CTAs of a decode call, and most CTAs times query rows of an item: what the
-// workspace has slots for (one CTA an SM for items of 128 rows, up to three for 16).
-constexpr int kDecodeCtas = 3 * 148, kDecodeRows = 48 * 148, kDecodeWideRows = pg::kWideRows * 148;
+// workspace has slots for, on up to kSms SMs (three CTAs an SM for items of 16 rows,
+// two for 32, one for 128; decode_stream checks each kernel's).
+constexpr int kSms = 148;
+constexpr int kDecodeCtas = 3 * kSms, kDecodeRows = 64 * kSms, kDecodeWideRows = pg::kWideRows * kSms;
+inline int decode_sms() { return std::min(sm_count(), kSms); }
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -107,7 +110,7 @@ attn_status_t decode_simt(const pg::DecodeArgs& a, const void* Q, const void* Kp
     const int smem = pg::simt_smem_bytes(a.d, a.dv);
     if (cudaFuncSetAttribute(pg::decode_simt, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    *grid = std::min(2 * sm_count(), kDecodeCtas);
+    *grid = 2 * decode_sms();
     return traced(ATTN_KERNEL_DECODE_SIMT, st, [&] {
         using T = __nv_bfloat16;
         pg::decode_simt<<<*grid, pg::kSimtThreads, smem, st>>>(a, static_cast<const T*>(Q), static_cast<const T*>(Kp),
@@ -138,9 +141,14 @@ attn_status_t decode_join(const pg::DecodeArgs& a, void* O, float* LSE, const pg
 // the element type, whose columns the maps' 128-byte rows hold. teams: 0, or one
 // team for each of so many items.
 template <typename C, typename T, typename Kern, typename... More>
-attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg::DecodeArgs& a, const void* Q,
-                            const void* Kp, const void* Vp, void* O, float* LSE, const pg::Parts& parts, int* grid,
-                            int teams, cudaStream_t st, const More&... more) {
+attn_status_t decode_stream(Kern kern, int kernel_id, pg::DecodeArgs& a, const void* Q, const void* Kp,
+                            const void* Vp, void* O, float* LSE, const pg::Parts& parts, int* grid, int teams,
+                            cudaStream_t st, const More&... more) {
+    static_assert(C::kCtasPerSm * kSms <= kDecodeCtas, "the workspace holds a head for each CTA");
+    static_assert(C::kCtasPerSm * C::kTileRows * kSms <= (C::kTileRows == pg::kWideRows ? kDecodeWideRows : kDecodeRows),
+                  "... and two pieces");
+    a.tile_rows = C::kTileRows;
+    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     CUtensorMap mk, mv;
     const int page = 1 << a.g.page_log2, heads = a.g.P * a.g.Hkv, box = std::min(page, pg::kTileKeys);
     constexpr auto type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -149,8 +157,7 @@ attn_status_t decode_stream(Kern kern, int kernel_id, int ctas_per_sm, const pg:
         return ATTN_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    *grid = teams > 0 ? teams * pg::kTeam
-                      : std::min(ctas_per_sm * sm_count(), std::min(kDecodeCtas, a.tile_rows == pg::kWideRows ? 148 : kDecodeRows / a.tile_rows));
+    *grid = teams > 0 ? teams * pg::kTeam : C::kCtasPerSm * decode_sms();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(*grid);
     cfg.blockDim = dim3(C::kThreads);
@@ -177,53 +184,49 @@ template <int DK, int DV, int R>
 attn_status_t decode_tc(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                         const pg::Parts& parts, int* grid, cudaStream_t st) {
     using C = pg::DecodeCfg<DK, DV, R, false>;
-    a.tile_rows = 16 * R;
-    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     if constexpr (R == 1) {
         // Teams where their CTAs are all resident at once and no sequence can be
         // longer than 8 tiles for each of a team's CTAs: one launch instead of two.
-        const long long items = 1ll * a.g.B * a.g.Hkv * a.row_tiles;
+        // (Up to 16 rows: one item a key head.)
+        const long long items = 1ll * a.g.B * a.g.Hkv;
         if (items * pg::kTeam <= C::kCtasPerSm * sm_count() &&
             (1ll * a.g.M << a.g.page_log2) <= 8 * pg::kTeam * pg::kTileKeys) {
             const attn_status_t s = decode_stream<pg::DecodeCfg<DK, DV, R, true>, __nv_bfloat16>(
-                pg::decode_tc<DK, DV, R, true>, ATTN_KERNEL_DECODE_TENSOR, C::kCtasPerSm, a, Q, Kp, Vp, O, LSE, parts,
-                grid, int(items), st);
+                pg::decode_tc<DK, DV, R, true>, ATTN_KERNEL_DECODE_TENSOR, a, Q, Kp, Vp, O, LSE, parts, grid,
+                int(items), st);
             *grid = 0;                                     // nothing to join
             return s;
         }
     }
-    return decode_stream<C, __nv_bfloat16>(pg::decode_tc<DK, DV, R, false>, ATTN_KERNEL_DECODE_TENSOR, C::kCtasPerSm,
-                                           a, Q, Kp, Vp, O, LSE, parts, grid, 0, st);
+    return decode_stream<C, __nv_bfloat16>(pg::decode_tc<DK, DV, R, false>, ATTN_KERNEL_DECODE_TENSOR, a, Q, Kp, Vp, O,
+                                           LSE, parts, grid, 0, st);
 }
 
 template <int DK, int DV>
 attn_status_t decode_wide(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                           const pg::Parts& parts, int* grid, cudaStream_t st) {
     using C = pg::DecodeWideCfg<DK, DV>;
-    a.tile_rows = pg::kWideRows;
-    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     CUtensorMap mq;
     if (!make_map_rows(&mq, Q, a.d, a.g.B * a.H * a.n, a.d, 64, pg::kWideRows)) return ATTN_ERR_CUDA;
-    return decode_stream<C, __nv_bfloat16>(pg::decode_wide<DK, DV>, ATTN_KERNEL_DECODE_WIDE, 1, a, Q, Kp, Vp, O, LSE,
-                                           parts, grid, 0, st, mq, static_cast<const __nv_bfloat16*>(Kp),
+    return decode_stream<C, __nv_bfloat16>(pg::decode_wide<DK, DV>, ATTN_KERNEL_DECODE_WIDE, a, Q, Kp, Vp, O, LSE, parts,
+                                           grid, 0, st, mq, static_cast<const __nv_bfloat16*>(Kp),
                                            static_cast<const __nv_bfloat16*>(Vp));
 }
 
 template <int DK, int DV, int RB, int R>
 attn_status_t decode_f32(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                          const pg::Parts& parts, int* grid, cudaStream_t st) {
-    using C = pg::DecodeF32Cfg<DK, DV, RB, R>;
-    a.tile_rows = RB * R;
-    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
-    return decode_stream<C, float>(pg::decode_f32<DK, DV, RB, R>, ATTN_KERNEL_DECODE_F32, C::kCtasPerSm, a, Q, Kp, Vp, O, LSE,
-                                   parts, grid, 0, st);
+    return decode_stream<pg::DecodeF32Cfg<DK, DV, RB, R>, float>(pg::decode_f32<DK, DV, RB, R>, ATTN_KERNEL_DECODE_F32, a,
+                                                                 Q, Kp, Vp, O, LSE, parts, grid, 0, st);
 }
 
 // Query rows of an item: as many of a key head's as there are, up to 128 (bf16,
 // tcgen05 above 32) or 16 (fp32), since every item reads its keys again. 8 x 32768
-// tokens, 32 rows: tcgen05 takes 172 us and mma.sync 196 at d = 128, 138 and 133 at d
-// = 64; 64 sequences of 100 to 3000 tokens, 24 rows: 83 and 76, 69 and 50; 200 of 30 to
-// 400, 20 rows, d = 128: 125 and 80. The host does not know the lengths.
+// tokens, 32 rows: tcgen05 takes 180 us and mma.sync 210 at d = 128, 140 and 105 at d
+// = 64; 64 sequences of 100 to 3000 tokens, 24 rows: 98 and 76, 73 and 42; 200 of 30 to
+// 400, 32 rows, d = 128: 115 and 82. At d = 128 the times cross with the lengths,
+// which the host does not know, and not with the rows: 20, 24, 28 and 32 are within
+// 4 % of each other.
 template <int DK, int DV>
 attn_status_t decode_rows(pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O, float* LSE,
                           const pg::Parts& parts, int* grid, bool f32, cudaStream_t st) {

@@ -196,3 +196,13 @@ def test_binding_refuses_before_the_library(L):
 
 def test_status_string_of_overlap(L):
     assert "overlap" in L.attn_status_string(9)
+
+
+def test_workspace_has_room_for_every_cta(L):
+    """Two pieces of an item for each of the CTAs that the GPU holds at once: on
+    each of 148 SMs three of 16 rows at d = dv = 64 and two of 32, two of 16 rows and
+    one of 32 at larger widths; a row is dv outputs, a maximum and a sum."""
+    sms, ask = 148, L.attn_decode_workspace_size
+    for rows, d, dv, ctas, tile in ((8, 64, 64, 3, 16), (24, 64, 64, 2, 32), (32, 48, 40, 2, 32), (16, 128, 128, 2, 16),
+                                    (17, 128, 128, 1, 32), (33, 128, 128, 1, 128)):
+        assert ask(4, rows, 1, 1, d, dv, 1) >= 2 * sms * ctas * tile * (dv + 2) * 4 + sms * ctas * 16, (rows, d, dv)
