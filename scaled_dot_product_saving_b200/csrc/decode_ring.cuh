@@ -101,7 +101,9 @@ __device__ __forceinline__ bool set_up(const Parts& parts, Ring<kStages, kGroups
 // tile of small pages takes many (16 of 16 tokens at d = 128): where a CTA has
 // an SM to itself, K and V have a warp each (8 sequences of 17000 tokens, 20
 // query rows, pages of 16: 123 us with one, 107 with two; in fp32, 4 rows of 32768
-// tokens, 191 and 167).
+// tokens, 191 and 167), and with two row groups also where two CTAs share it (d =
+// 64: 8 x 16500 tokens, 24 rows, pages of 64: 63.7 us with one, 60.0 with two; 4 x
+// 28000, 21 rows, pages of 8: 77.1 and 64.4; 200 of 30 to 400, 20 rows: 40.5 and 41.1).
 enum class Loads { kBoth, kKeys, kValues };
 
 // A producer warp; the one of K, or of both, leads. A tile is 64 / box pages (box
