@@ -336,8 +336,8 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  *  - page is a power of two, 8 to 256; d, dv <= 128 (ATTN_ERR_UNSUPPORTED
  *    beyond) with rows of whole 16 bytes (multiples of 8 in bf16, of 4 in
  *    fp32; ATTN_ERR_SHAPE otherwise). num_pages * Hkv and B * max_pages are
- *    below 2^31, num_pages, max_pages * page and (attn_decode) B * H * n at
- *    most 2^30.
+ *    below 2^31, num_pages and max_pages * page at most 2^30 (ATTN_ERR_SHAPE
+ *    beyond, as for the limits of single calls that are given there).
  *  - Nothing is read back to the host: every call can be captured in a graph
  *    and replayed. What a call finds on the device is checked there. Lengths
  *    are clamped to [0, max_pages * page]. A page number outside
@@ -379,6 +379,9 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  * weight, and for no other. H must be a multiple of Hkv.
  * Pieces of a long sequence are joined in a fixed order: a repeated call gives
  * the same bits. Whole prompts belong to attn_fwd.
+ * B * H * n is at most 2^30, and the key tiles of a call (64 tokens, at most
+ * ceil(H / Hkv * n / 16) * (max_pages * page / 64 + 3) for each sequence and key
+ * head) are below 2^51. The workspace size is 0 if an argument is invalid.
  */
 size_t attn_decode_workspace_size(int B, int H, int Hkv, int n, int d, int dv, attn_dtype_t dtype);
 attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_pages, const int* table,
@@ -387,7 +390,8 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
                           int num_pages, int page, int max_pages, attn_dtype_t dtype, int causal,
                           float scale, void* stream);
 
-/* Workspace of attn_cache_append, _fork and _compact. 0 if a size is invalid. */
+/* Workspace of attn_cache_append, _fork and _compact. 0 if a size is one that
+ * they refuse whatever the page (max_pages is at most 2^27 then). */
 size_t attn_cache_workspace_size(int B, int max_pages, int num_pages);
 
 /*
@@ -395,7 +399,7 @@ size_t attn_cache_workspace_size(int B, int max_pages, int num_pages);
  *   K [B,Hkv,n,d], V [B,Hkv,n,dv]: the keys and values that attn_fwd or
  *   attn_decode takes. Rows i < new_len[b] (clamped to [0, n]; NULL: n) become
  *   tokens lens[b] + i; the others are padding. Pages are taken for sequence
- *   0 first, then 1, and so on.
+ *   0 first, then 1, and so on. B * Hkv * n is below 2^30.
  */
 attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, void* V_pages,
                                 const int* table, const int* lens, const int* ref, const int* new_len,
@@ -414,7 +418,7 @@ attn_status_t attn_cache_append(const void* K, const void* V, void* K_pages, voi
  * has one holder: it stays with the sequence it belonged to (else with the
  * lowest of those that continue it) if nothing else refers to it, and is
  * copied to a fresh page for every other. Entries of table_out that a sequence
- * gives up are -1.
+ * gives up are -1. B is at most 2^29.
  */
 attn_status_t attn_cache_fork(void* K_pages, void* V_pages, const int* table, const int* lens,
                               const int* ref, const int* src, const int* keep, int* table_out,

@@ -42,6 +42,19 @@ bool apart(const Region (&written)[W], const Region (&read)[R], const Region* in
     return true;
 }
 
+// Widths of a row, which is whole 16 bytes.
+attn_status_t check_widths(int d, int dv, attn_dtype_t dtype) {
+    if (d > pg::kMaxWidth || dv > pg::kMaxWidth) return ATTN_ERR_UNSUPPORTED;
+    const int es = dtype == ATTN_F32 ? 4 : 2;
+    return d * es % 16 || dv * es % 16 ? ATTN_ERR_SHAPE : ATTN_OK;
+}
+
+// Kernels number pages, tokens and what lies a tile or a block past them in 32 bits.
+bool books_fit(int B, int max_pages, int num_pages, int page_log2) {
+    return num_pages <= (1 << 30) && static_cast<long long>(B) * max_pages < (1ll << 31) &&
+           max_pages <= ((1 << 30) >> page_log2);
+}
+
 attn_status_t check_cache(int B, int Hkv, int d, int dv, int num_pages, int page, int max_pages,
                           attn_dtype_t dtype, pg::Geometry* g) {
     if (dtype != ATTN_F32 && dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
@@ -50,12 +63,9 @@ attn_status_t check_cache(int B, int Hkv, int d, int dv, int num_pages, int page
     int log2 = 0;
     while ((1 << log2) < page && log2 < 30) ++log2;
     if ((1 << log2) != page || log2 < pg::kMinPageLog2 || log2 > pg::kMaxPageLog2) return ATTN_ERR_UNSUPPORTED;
-    if (d > pg::kMaxWidth || dv > pg::kMaxWidth) return ATTN_ERR_UNSUPPORTED;
-    const int es = dtype == ATTN_F32 ? 4 : 2;
-    if (d * es % 16 || dv * es % 16) return ATTN_ERR_SHAPE;
-    // Kernels number pages, tokens and what lies a tile or a block past them in 32 bits.
-    if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || num_pages > (1 << 30) ||
-        static_cast<long long>(B) * max_pages >= (1ll << 31) || max_pages > ((1 << 30) >> log2))
+    const attn_status_t widths = check_widths(d, dv, dtype);
+    if (widths != ATTN_OK) return widths;
+    if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || !books_fit(B, max_pages, num_pages, log2))
         return ATTN_ERR_SHAPE;
     *g = pg::Geometry{B, max_pages, num_pages, Hkv, log2};
     return ATTN_OK;
@@ -101,8 +111,7 @@ attn_status_t check_decode(int B, int H, int Hkv, int n, int d, int dv, attn_dty
     if (dtype != ATTN_F32 && dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
     if (B < 1 || H < 1 || Hkv < 1 || n < 1 || d < 1 || dv < 1 || H % Hkv) return ATTN_ERR_SHAPE;
     if (static_cast<double>(B) * H * n > 1073741824.0) return ATTN_ERR_SHAPE;
-    if (d > pg::kMaxWidth || dv > pg::kMaxWidth) return ATTN_ERR_UNSUPPORTED;
-    return ATTN_OK;
+    return check_widths(d, dv, dtype);
 }
 
 attn_status_t decode_simt(const pg::DecodeArgs& a, const void* Q, const void* Kp, const void* Vp, void* O,
@@ -377,7 +386,7 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
 }
 
 size_t attn_cache_workspace_size(int B, int max_pages, int num_pages) {
-    if (B < 1 || max_pages < 1 || num_pages < 1 || static_cast<long long>(B) * max_pages >= (1ll << 31)) return 0;
+    if (B < 1 || max_pages < 1 || num_pages < 1 || !books_fit(B, max_pages, num_pages, pg::kMinPageLog2)) return 0;
     return carve_cache(B, max_pages, num_pages).total;
 }
 

@@ -206,3 +206,32 @@ def test_workspace_has_room_for_every_cta(L):
     for rows, d, dv, ctas, tile in ((8, 64, 64, 3, 16), (24, 64, 64, 2, 32), (32, 48, 40, 2, 32), (16, 128, 128, 2, 16),
                                     (17, 128, 128, 1, 32), (33, 128, 128, 1, 128)):
         assert ask(4, rows, 1, 1, d, dv, 1) >= 2 * sms * ctas * tile * (dv + 2) * 4 + sms * ctas * 16, (rows, d, dv)
+
+
+def test_workspace_size_is_zero_for_what_every_call_refuses(L):
+    big = 1 << 30
+    assert L.attn_cache_workspace_size(1, 1, big + 1) == 0 < L.attn_cache_workspace_size(1, 1, big)
+    assert L.attn_cache_workspace_size(1, (big >> 3) + 1, 1) == 0 < L.attn_cache_workspace_size(1, big >> 3, 1)
+    for d, dv, dtype in ((60, 64, 1), (64, 4, 1), (62, 64, 0), (64, 2, 0), (136, 64, 1)):
+        assert L.attn_decode_workspace_size(1, 8, 2, 1, d, dv, dtype) == 0, (d, dv, dtype)
+    assert L.attn_decode_workspace_size(1, 1, 1, big + 1, 64, 64, 1) == 0
+
+
+def test_limits_of_single_calls(L):
+    """At a limit a call goes on to the launch, past it it is refused."""
+    def at(f, status, **change):
+        if status != OK_ON_CPU or not torch.cuda.is_available():
+            assert f(L, wsb=1 << 45, **change) == status, change
+
+    def far(**sizes):                                     # pools and rows that do not meet
+        names = ("k", "v", "kp", "vp", "table", "lens", "ref", "new_len", "table_out", "lens_out", "ref_out",
+                 "info", "ws", "src", "keep")
+        return {**sizes, **{x: ctypes.c_void_p((i + 1) << 48) for i, x in enumerate(names)}}
+
+    app = lambda **s: {k: v for k, v in far(**s).items() if k not in ("src", "keep")}
+    frk = lambda **s: {k: v for k, v in far(**s).items() if k not in ("k", "v", "new_len")}
+    at(append, OK_ON_CPU, **app(B=1, Hkv=1, n=(1 << 30) - 1, d=8, dv=8))
+    at(append, 2, **app(B=1, Hkv=1, n=1 << 30, d=8, dv=8))
+    at(append, 2, **app(B=1 << 10, Hkv=1 << 10, n=1 << 10, d=8, dv=8))
+    at(fork, OK_ON_CPU, **frk(B=1 << 29, M=1))
+    at(fork, 2, **frk(B=(1 << 29) + 1, M=1))
