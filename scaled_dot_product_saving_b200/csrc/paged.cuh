@@ -116,6 +116,20 @@ __device__ __forceinline__ long long divide(long long x, long long y) {
     return x / y;
 }
 
+// The sequence in [b0, b1) that holds unit pos, *x being the units before b0 and
+// then those before it. The last one if none does, which only lengths that change
+// during the call can bring about: they must not lead past the arrays.
+template <typename Units>
+__device__ __forceinline__ int sequence_of(Units&& units, int b0, int b1, long long pos, long long* x) {
+    int b = b0;
+    for (; b < b1 - 1; ++b) {
+        const long long u = units(b);
+        if (pos < *x + u) break;
+        *x += u;
+    }
+    return b;
+}
+
 // A CTA's share, walked by one warp (all lanes hold the same walker). With
 // total = q * ctas + r, the first r CTAs take q + 1 units and the others q.
 struct Walker {
@@ -153,13 +167,7 @@ struct Walker {
         const bool mine = left > 0 && pos >= before && pos < inc;
         int found = 0;
         long long x = before;
-        if (mine) {
-            for (found = b0;; ++found) {
-                const long long u = units_of(a, found);
-                if (pos < x + u) break;
-                x += u;
-            }
-        }
+        if (mine) found = sequence_of([&](int k) { return units_of(a, k); }, b0, b1, pos, &x);
         const unsigned who = __ballot_sync(0xffffffffu, mine);
         const int from = who ? __ffs(who) - 1 : 0;
         b = __shfl_sync(0xffffffffu, found, from);
@@ -194,10 +202,10 @@ struct Walker {
         return false;
     }
 
-    // The CTA that takes unit x.
+    // The CTA that takes unit x; never one that the call does not have.
     __device__ int owner(long long x) const {
-        const long long longer = r * (q + 1);
-        return int(x < longer ? divide(x, q + 1) : r + divide(x - longer, q));
+        const long long longer = r * (q + 1), c = x < longer ? divide(x, q + 1) : r + divide(x - longer, q);
+        return c < ctas ? int(c) : ctas - 1;
     }
 };
 
