@@ -202,7 +202,7 @@ decode_join(DecodeArgs a, T* __restrict__ O, float* __restrict__ LSE, Parts part
     const int hk = h.item / a.row_tiles, r0 = (h.item % a.row_tiles) * a.tile_rows;
     const int r = (blockIdx.y * (kJoinThreads / 32) + warp) / split, part = warp % split;
     const bool live = r < min(a.tile_rows, a.rows - r0) && (r0 + r) % a.n < h.nq;
-    const int first = blockIdx.x, pieces = h.last - first + 1;
+    const int first = blockIdx.x, pieces = pieces_of(h, first, gridDim.x);
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {

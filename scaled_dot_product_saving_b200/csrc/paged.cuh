@@ -202,10 +202,10 @@ struct Walker {
         return false;
     }
 
-    // The CTA that takes unit x; never one that the call does not have.
+    // The CTA that takes unit x.
     __device__ int owner(long long x) const {
-        const long long longer = r * (q + 1), c = x < longer ? divide(x, q + 1) : r + divide(x - longer, q);
-        return c < ctas ? int(c) : ctas - 1;
+        const long long longer = r * (q + 1);
+        return int(x < longer ? divide(x, q + 1) : r + divide(x - longer, q));
     }
 };
 
@@ -249,6 +249,12 @@ struct Head {
     int last;               // last CTA that holds a piece of it
     int nq;
 };
+// How many pieces the item has that starts in CTA first of ctas. (None past the
+// slots, should lengths have changed during the call. Bounded here, once an item
+// and row: in owner() it cost fp32 with 8 rows at d = 128 2 %.)
+__device__ __forceinline__ int pieces_of(const Head& h, int first, int ctas) {
+    return max(0, min(h.last, ctas - 1) - first + 1);
+}
 struct Parts {
     float* o;               // [2G][tile_rows][dv], not divided by l
     float* ml;              // [2G][tile_rows][2]: maximum (base 2) and sum

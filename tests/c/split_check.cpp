@@ -99,6 +99,7 @@ int main() {
             const Piece& f = v[0].first;
             CHECK(f.t0 == 0 && v.back().first.t1 == f.tiles && f.tiles == tiles_of(lens[f.b]));
             CHECK(v[0].second.last == v.back().second.cta);
+            CHECK(pieces_of(Head{f.b, it.first.second, v[0].second.last, f.nq}, v[0].second.cta, gridDim.x) == int(v.size()));
             for (size_t i = 1; i < v.size(); ++i)
                 CHECK(v[i].first.t0 == v[i - 1].first.t1 && v[i].second.cta == v[i - 1].second.cta + 1);
         }
@@ -115,7 +116,8 @@ int main() {
             while (w.next(a, &p)) {
                 const int last = w.owner(p.end - 1);
                 CHECK(p.b < B && p.item < a.g.Hkv * a.row_tiles && p.t0 < p.t1 && p.t1 <= p.tiles);
-                CHECK(last >= 0 && last < gridDim.x);
+                const int pieces = pieces_of(Head{p.b, p.item, last, p.nq}, blockIdx.x, gridDim.x);
+                CHECK(pieces >= 0 && blockIdx.x + pieces <= gridDim.x);
             }
             CHECK(w.b <= B && reads_past == 0);
         }
