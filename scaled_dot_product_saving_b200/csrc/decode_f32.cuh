@@ -243,14 +243,10 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 }
                 const int k0 = tile0 + k8;
                 const bool whole = there == 0xffu && k0 + 8 <= see_all;
-                unsigned hidden = 0;                       // rows (a bit a set) that do not see the key
                 if (!whole) {
 #pragma unroll
                     for (int x = 0; x < kSets; ++x)
-                        if (!(there >> my_key & 1) || k0 + my_key >= see[x]) {
-                            sc[x] = -INFINITY;
-                            hidden |= 1u << x;
-                        }
+                        if (!(there >> my_key & 1) || k0 + my_key >= see[x]) sc[x] = -INFINITY;
                 }
                 // Running maximum over the keys of a row (lanes that differ in bits
                 // 2, 3 and 4); the reference moves when it has grown by more than 8.
@@ -285,7 +281,12 @@ decode_f32(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUte
                 for (int x = 0; x < kSets; ++x) {
                     const float e = exp2f(sc[x] - (m[x] == -INFINITY ? 0.f : m[x]));
                     l[x] += e;
-                    weights[my_key * RB + 4 * x + my_row] = hidden >> x & 1 ? -0.f : e;
+                    weights[my_key * RB + 4 * x + my_row] = e;
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int x = 0; x < kSets; ++x)
+                        if (!(there >> my_key & 1) || k0 + my_key >= see[x]) weights[my_key * RB + 4 * x + my_row] = -0.f;
                 }
                 __syncwarp();
 #pragma unroll
