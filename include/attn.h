@@ -379,9 +379,10 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  * weight, and for no other. H must be a multiple of Hkv.
  * Pieces of a long sequence are joined in a fixed order: a repeated call gives
  * the same bits. Whole prompts belong to attn_fwd.
- * B * H * n is at most 2^30, and the key tiles of a call (64 tokens, at most
- * ceil(H / Hkv * n / 16) * (max_pages * page / 64 + 3) for each sequence and key
- * head) are below 2^51. The workspace size is 0 if an argument is invalid.
+ * scale * log2(e) must be finite. B * H * n is at most 2^30, and the key tiles
+ * of a call (64 tokens; ceil(H / Hkv * n / 16) * (max_pages * page / 64 + 3) for
+ * each sequence and key head) are below 2^51. The workspace size is 0 if an
+ * argument is invalid.
  */
 size_t attn_decode_workspace_size(int B, int H, int Hkv, int n, int d, int dv, attn_dtype_t dtype);
 attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_pages, const int* table,

@@ -340,7 +340,7 @@ attn_status_t attn_decode(const void* Q, const void* K_pages, const void* V_page
     attn_status_t s = check_decode(B, H, Hkv, n, d, dv, dtype);
     if (s == ATTN_OK) s = check_cache(B, Hkv, d, dv, num_pages, page, max_pages, dtype, &g);
     if (s != ATTN_OK) return s;
-    if (!std::isfinite(scale)) return ATTN_ERR_SHAPE;
+    if (!std::isfinite(scale * kLog2e)) return ATTN_ERR_SHAPE;      // the kernels' factor: base 2
     if (!Q || !K_pages || !V_pages || !table || !lens || !O || !LSE) return ATTN_ERR_NULL;
     if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O) || !aligned16(LSE) ||
         !aligned4(table) || !aligned4(lens) || !aligned4(q_len))

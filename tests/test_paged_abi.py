@@ -235,3 +235,12 @@ def test_limits_of_single_calls(L):
     at(append, 2, **app(B=1 << 10, Hkv=1 << 10, n=1 << 10, d=8, dv=8))
     at(fork, OK_ON_CPU, **frk(B=1 << 29, M=1))
     at(fork, 2, **frk(B=(1 << 29) + 1, M=1))
+
+
+def test_scale_whose_factor_in_base_two_is_not_finite(L):
+    """Scores are taken in base 2: a scale that overflows there would make a score of
+    zero one that is not a number."""
+    for scale in (2.4e38, 3.4e38, -3e38):
+        assert decode(L, scale=scale) == 2
+    if not torch.cuda.is_available():
+        assert decode(L, scale=2.3e38) == OK_ON_CPU and decode(L, scale=-2.3e38) == OK_ON_CPU
