@@ -201,8 +201,9 @@ size_t attn_bwd_noalloc_scratch_bytes(void);
 
 /*
  * attn_get_device_error -- synchronise `stream`, then report and clear the
- * device-side error word of the current device. Every wait inside the
- * tensor-core kernels is bounded; a wait that runs out writes
+ * device-side error word of the current device. Every wait of the tensor-core
+ * kernels, and of attn_decode's, on a copy, a product or another warp is
+ * bounded; a wait that runs out writes
  * ATTN_ERR_DEVICE_TIMEOUT there, and the kernel releases its tensor memory
  * and exits instead of hanging. The word is sticky: while it is set, the
  * tensor-core kernels skip their work, so outputs of calls made after a
@@ -377,6 +378,11 @@ attn_status_t attn_outproj_bwd(const void* O, const void* Wo, const void* G, voi
  * hold (NaN included) has no influence; an infinite or NaN value of a token makes
  * its column of O infinite or NaN for every query that sees it, however small the
  * weight, and for no other. H must be a multiple of Hkv.
+ * Scores, maxima, sums and unfinished outputs are fp32. In bf16 the tensor-core
+ * kernels, like attn_fwd, round the weights exp(S - m) to bf16 for the product
+ * with V (half a step, 2^-8 of each; their sum is of the unrounded ones), which
+ * adds up to 2^-8 sum_j P_ij |v_j| to the rounding of O; ATTN_PATH_SIMT keeps
+ * them in fp32.
  * Pieces of a long sequence are joined in a fixed order: a repeated call gives
  * the same bits. Whole prompts belong to attn_fwd.
  * scale * log2(e) must be finite. B * H * n is at most 2^30, and the key tiles

@@ -8,8 +8,9 @@
 // consumers need: which keys are there, and with the first tile of a piece the
 // piece, and where a kernel asks for it the query rows.
 //
-// Every wait is bounded and on an mbarrier. One that runs out sets the abort
-// flag, which ends every other wait, and each warp leaves its loop.
+// Every wait in the ring is bounded and on an mbarrier. One that runs out sets the
+// abort flag, which ends every other wait, and each warp leaves its loop; the block
+// and cluster barriers behind the loops are reached on every way.
 #pragma once
 
 #include "decode.cuh"
@@ -52,7 +53,8 @@ __device__ __forceinline__ bool ring_wait(RingT& ring, uint64_t* bar, uint32_t p
         const long long from = clock64();
         for (uint32_t turn = 1; !ok; ++turn) {
             ok = mbar_try_wait(at, parity);
-            // Two cycles a nanosecond: no SM clock is above 2 GHz.
+            // Two cycles a nanosecond: no SM clock is above 2 GHz. (At a lower clock
+            // the bound is longer by as much.)
             if (!ok && (turn & 15u) == 0u && (*abort || (unsigned long long)(clock64() - from) > 2 * budget_ns)) break;
         }
     }
