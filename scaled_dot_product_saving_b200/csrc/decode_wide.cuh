@@ -16,9 +16,10 @@
 // ones. (What bounded the kernel with one issuing warp was that warp: two waits,
 // twelve MMAs and a message to the stream, 1,900 cycles a tile.)
 //
-// One B200, 8 sequences of 32768 tokens, 8 key heads, d = 128: 64 rows 186 us, 128
-// rows 205 (5.8 and 5.2 TB/s). 8 of 16384 to 32768 tokens, 16 key heads, d = 64, 48
-// rows: 228 us (3.4 TB/s); a tile has half the bytes, and the softmax bounds it.
+// One B200, 8 sequences of 32768 tokens, 8 key heads, d = 128: 64 rows 186 to
+// 220 us, 128 rows 205 to 250 (5.8 and 5.2 TB/s at best; runs differ). 8 of 16384 to
+// 32768 tokens, 16 key heads, d = 64, 48 rows: 200 to 246 us (3.9 TB/s at best): a tile
+// has half the bytes, and the softmax of one CTA an SM does not keep up.
 #pragma once
 
 #include "decode_ring.cuh"
