@@ -156,13 +156,14 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     __shared__ uint64_t left[kSlots];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    __shared__ float2 team_ml[kTeamed ? 16 : 1];          // maximum and sum of each row, for the team
+    __shared__ float2 team_ml[kTeamed ? 16 : 1];          // maximum and sum of each row, for the team; a sum
+                                                          // below zero: the CTA had no tile
 
     std::conditional_t<kTeamed, Member, Walker> w;
     if (kTeamed || (warp >= kKeys && warp < kKeys + C::kProducers)) w.start(a);   // while the barriers are set up
     if (threadIdx.x == 0)
         for (int x = 0; x < kSlots; ++x) mbar_init(&left[x], kKeys);
-    if (kTeamed && threadIdx.x < 16) team_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    if (kTeamed && threadIdx.x < 16) team_ml[threadIdx.x] = make_float2(-INFINITY, -1.f);   // until it has a tile's
     const bool going = set_up<kTeamed>(parts, ring, smem, kKeys + (C::kJoiner ? 1 : 0), C::kProducers);   // fences the barriers' initialisation
     if (!kTeamed && !going) return;
 
@@ -605,7 +606,7 @@ decode_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             const float Z = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) {
-                if (x[k].y == 0.f) continue;              // no keys there: its output may not be written
+                if (x[k].y < 0.f) continue;               // no tile there: its output is not written
                 const float f = ex2(x[k].x - Z);
                 L = fmaf(x[k].y, f, L);
                 y0 = fmaf(y[k].x, f, y0);

@@ -592,3 +592,25 @@ def test_after_a_timeout_nothing_is_written(dt, room, H):
     assert lib.attn_get_device_error() == lib.ATTN_ERR_DEVICE_TIMEOUT
     assert (out == 7).all() and (lse == 7).all()
     compare(*run(dev, q, out=out, lse=lse), dt, host, q)
+
+
+@SPLITS
+@KERNELS
+def test_values_not_finite_where_every_score_is_minus_infinity(dt, H, path, room):
+    """Zero weights alone: zero times an infinite value is not zero."""
+    rng = np.random.default_rng(27)
+    lens = (70, 700, 1)
+    c = numpy_cache(rng, 3, 1, 16, 64, 64, lens, M=width(lens, 16, room))
+    c["k_pages"][..., 7] = -np.inf
+    for b, L in enumerate(lens):
+        c["v_pages"][c["table"][b, (L - 1) // 32], 0, 0, 5] = np.inf
+    q = rng.standard_normal((3, H, 1, 64))
+    q[..., 7] = 1.0
+    q = torch.tensor(q, device="cuda").to(DT[dt])
+    try:
+        lib.attn_set_path(getattr(lib, f"ATTN_PATH_{path}"))
+        o, lse = run(on_gpu(c, dt)[0], q)
+        assert torch.isnan(o[..., 5]).all() and torch.isneginf(lse).all()
+        assert (o[..., [x for x in range(64) if x != 5]] == 0).all()
+    finally:
+        lib.attn_set_path(lib.ATTN_PATH_AUTO)
